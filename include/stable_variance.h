@@ -346,6 +346,106 @@ sv_status sv_adn_sum_f32(const float *x, int64_t n, int fold, float *out, void *
                          void *stream);
 
 /*
+ * Element types of the layer norm and the embedding (the reductions above
+ * name theirs in their suffix).  16-bit values are converted to float32 as
+ * they are read, everything is computed in float32 (each operation rounded
+ * on its own, as above), and each output is rounded once, to nearest even.
+ */
+#define SV_DTYPE_F32 0
+#define SV_DTYPE_BF16 1
+#define SV_DTYPE_F16 2
+
+/*
+ * Layer norm of each row of the [rows, n] matrix x (row r starts at
+ * x + r * ldx values):
+ *   m1 = x_0 + Sum(x_i - x_0) / n,  d_i = x_i - m1,  b = Sum(d_i) / n
+ *   var = max(Sum(d_i^2) / n - b^2, 0),  mean = m1 + b,
+ *   rstd = 1 / sqrt(var + eps)            (rounded from double)
+ *   y_i = ((d_i - b) * rstd) * weight_i + bias_i
+ * the shift, centring and two-term correction of sv_variance_f32 with ddof
+ * 0; the sums are pairwise or compensated sums whose order is fixed by n and
+ * dtype, so that a row's outputs have the same bits on every run and do not
+ * depend on the other rows.  A row of equal values gives y = bias exactly
+ * when eps > 0 (eps = 0 divides zero by zero: NaN).  An Inf or NaN in a row
+ * makes that row NaN and no other.  As in sv_variance_f32, a row whose
+ * squared spread overflows float32 has var = Inf (then rstd = 0).
+ *   dtype        SV_DTYPE_* of x and y
+ *   weight, bias n values of param_dtype each (dtype or SV_DTYPE_F32), each
+ *                may be NULL (then 1 and 0)
+ *   eps          >= 0 and finite
+ *   y            [rows, n] of dtype, row stride ldy; must not overlap x
+ *   mean, rstd   rows float32 values each, each may be NULL
+ * Row strides are in values, at least n; x and y need only the alignment of
+ * their type (16-byte aligned rows are the fastest).  n == 0 gives mean =
+ * rstd = NaN.  n <= 2^27, rows * n <= 2^36 and strides * rows <= 2^40, else
+ * SV_ERR_UNSUPPORTED.  No workspace.
+ */
+sv_status sv_layer_norm(const void *x, int dtype, int64_t rows, int64_t n, int64_t ldx, const void *weight,
+                        const void *bias, int param_dtype, double eps, void *y, int64_t ldy, float *mean, float *rstd,
+                        void *stream);
+
+/*
+ * Gradient of the layer norm at x, for the gradient dy of y and the mean and
+ * rstd that sv_layer_norm wrote.  With d_i = x_i - mean, b = Sum(d_i) / n
+ * (what the rounded mean is off by), xhat_i = (d_i - b) * rstd and
+ * g_i = dy_i * weight_i:
+ *   dx_i = rstd * ((g_i - Sum(g) / n) - xhat_i * c),
+ *          c = rstd * (Sum(g_i d_i) - b * Sum(g)) / n
+ *   dweight_j = sum over the rows of dy_j * xhat_j
+ *   dbias_j = sum over the rows of dy_j
+ * Every sum's order is fixed by the shape and dtype: the same bits on every
+ * run, no atomics.
+ *   dtype          SV_DTYPE_* of dy, x and dx; strides as for sv_layer_norm
+ *   weight         may be NULL (then 1)
+ *   param_dtype    type of weight, dweight and dbias: dtype or SV_DTYPE_F32
+ *   dx, dweight, dbias  each may be NULL: that gradient is not computed.
+ *                  With rows == 0, dweight and dbias are set to zero.  dx
+ *                  must not overlap dy or x
+ *   workspace      sv_layer_norm_backward_workspace_size(rows, n, dtype)
+ *                  bytes, 256-byte aligned scratch (no initialisation, nothing
+ *                  kept); may be NULL when dweight and dbias are NULL or the
+ *                  size is 0
+ * Limits as for sv_layer_norm ((size_t)-1 beyond them).
+ */
+size_t sv_layer_norm_backward_workspace_size(int64_t rows, int64_t n, int dtype);
+sv_status sv_layer_norm_backward(const void *dy, int64_t lddy, const void *x, int64_t ldx, int dtype, int64_t rows,
+                                 int64_t n, const void *weight, int param_dtype, const float *mean, const float *rstd,
+                                 void *dx, int64_t lddx, void *dweight, void *dbias, void *workspace,
+                                 size_t workspace_bytes, void *stream);
+
+/*
+ * Embedding lookup: out[t] = scale * table[ids[t]] for each of `tokens`
+ * tokens, the float32 product rounded to dtype.  table is [vocab, dim] with row
+ * stride ldt, out [tokens, dim] with row stride ldo (in values, at least
+ * dim).  ids: int32 (id_bytes 4) or int64 (id_bytes 8).  An id outside
+ * [0, vocab) reads nothing and gives a row of NaN.  out must not overlap
+ * table.  tokens <= 2^30, vocab <= 2^31 - 2, dim <= 2^27, tokens * dim and
+ * vocab * dim <= 2^36, strides times rows <= 2^40, else SV_ERR_UNSUPPORTED.
+ * No workspace.
+ */
+sv_status sv_embedding(const void *ids, int id_bytes, int64_t tokens, const void *table, int dtype, int64_t vocab,
+                       int64_t dim, int64_t ldt, float scale, void *out, int64_t ldo, void *stream);
+
+/*
+ * Gradient of the embedding's table: grad[v] = scale * (sum of dy[t] over
+ * the tokens with ids[t] == v), every row of grad ([vocab, dim], row stride
+ * ldg) written, rows without tokens as +0.  The tokens are sorted by id
+ * first (stable); a row's sum is a compensated sum in token order (TwoSum,
+ * the errors in a carry), cut into runs of tokens that depend on that row's
+ * tokens alone, so the bits are the same on every run.  Ids outside
+ * [0, vocab) and ids equal to `padding` (-1: none) take no part.
+ *   dtype      SV_DTYPE_* of dy ([tokens, dim], row stride lddy) and grad
+ *   workspace  sv_embedding_backward_workspace_size(tokens, vocab, dim,
+ *              dtype) bytes, 256-byte aligned scratch (no initialisation,
+ *              nothing kept); NULL allowed when that size is 0
+ * Limits as for sv_embedding ((size_t)-1 beyond them).
+ */
+size_t sv_embedding_backward_workspace_size(int64_t tokens, int64_t vocab, int64_t dim, int dtype);
+sv_status sv_embedding_backward(const void *dy, int64_t lddy, const void *ids, int id_bytes, int64_t tokens,
+                                int dtype, int64_t vocab, int64_t dim, float scale, int64_t padding, void *grad,
+                                int64_t ldg, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
  * Measurement aid, not part of the method: reads x[0 .. n) once from HBM with
  * plain non-temporal 16-byte loads (x 16-byte aligned, n <= 2^36) and does no
  * arithmetic of the method, so its duration is the practical read ceiling

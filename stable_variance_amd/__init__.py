@@ -10,6 +10,12 @@ no GPU is visible, the calls raise.
     var(x, dim=-1, ddof=0, return_mean=False)
                                    -> per-slice variance (and mean) of a 2-D
                                       (or 1-D) float32 tensor
+    layer_norm(x, weight, bias), layer_norm_backward(...)
+                                   -> layer norm of rows on the variance's
+                                      statistics, and its gradients
+    embedding(ids, table, scale), embedding_backward(...)
+                                   -> rows of a table, and the table's
+                                      gradient as compensated sums by token
 
 Method: Pennacchio, "Variance in float32 with a first-element shift, a local
 centring and a compensated tree sum", §2 steps 1-4.
@@ -22,7 +28,8 @@ import threading
 
 from .build import LIB as _LIB_PATH
 
-__all__ = ["tree_sum", "var", "var_variant", "capi", "library_path", "SvError", "set_tuning", "VARIANTS"]
+__all__ = ["tree_sum", "var", "var_variant", "capi", "library_path", "SvError", "set_tuning", "VARIANTS",
+           "layer_norm", "layer_norm_backward", "embedding", "embedding_backward"]
 
 SV_OK = 0
 _STATUS = {1: "SV_ERR_INVALID_ARGUMENT", 2: "SV_ERR_WORKSPACE", 3: "SV_ERR_NO_DEVICE", 4: "SV_ERR_HIP",
@@ -101,6 +108,21 @@ def capi():
                 L.sv_adn_sum_f32_workspace_size.argtypes = [i64]
                 L.sv_adn_sum_f32.restype = ctypes.c_int
                 L.sv_adn_sum_f32.argtypes = [vp, i64, ctypes.c_int, vp, vp, sz, vp]
+                cint = ctypes.c_int
+                L.sv_layer_norm.restype = cint
+                L.sv_layer_norm.argtypes = [vp, cint, i64, i64, i64, vp, vp, cint, ctypes.c_double, vp, i64, vp, vp, vp]
+                L.sv_layer_norm_backward_workspace_size.restype = sz
+                L.sv_layer_norm_backward_workspace_size.argtypes = [i64, i64, cint]
+                L.sv_layer_norm_backward.restype = cint
+                L.sv_layer_norm_backward.argtypes = [vp, i64, vp, i64, cint, i64, i64, vp, cint, vp, vp, vp, i64, vp,
+                                                     vp, vp, sz, vp]
+                L.sv_embedding.restype = cint
+                L.sv_embedding.argtypes = [vp, cint, i64, vp, cint, i64, i64, i64, ctypes.c_float, vp, i64, vp]
+                L.sv_embedding_backward_workspace_size.restype = sz
+                L.sv_embedding_backward_workspace_size.argtypes = [i64, i64, i64, cint]
+                L.sv_embedding_backward.restype = cint
+                L.sv_embedding_backward.argtypes = [vp, i64, vp, cint, i64, cint, i64, i64, ctypes.c_float, i64, vp, i64,
+                                                    vp, sz, vp]
                 L.sv_probe_read_bandwidth.restype = ctypes.c_int
                 L.sv_probe_read_bandwidth.argtypes = [vp, i64, vp, vp]
                 _lib = L
@@ -317,3 +339,12 @@ def var_variant(x, variant, dim: int = -1, ddof: int = 0, return_mean: bool = Fa
                                             mean.data_ptr() if (mean is not None and ns) else None,
                                             ws.data_ptr() if ws is not None else None, need, stream))
     return (out, mean) if return_mean else out
+
+
+def __getattr__(name):
+    # the autograd functions need torch at import time, the rest only in use
+    if name in ("layer_norm", "layer_norm_backward", "embedding", "embedding_backward"):
+        from . import layers
+
+        return getattr(layers, name)
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -1,0 +1,306 @@
+// Layer norm over the rows of a matrix, forward and backward, on gfx950.
+//
+// Forward, for a row x of n values (all in float32):
+//   m1  = fl(x_0 + sum(x_i - x_0) / n)          shift by the first value
+//   d_i = x_i - m1,  b = sum(d_i) / n           local centring; b is what m1
+//                                               is off by
+//   var = max(sum(d_i^2) / n - b^2, 0)          two-term correction
+//   mean = m1 + b,  rstd = 1 / sqrt(var + eps)
+//   y_i = (d_i - b) * rstd * w_i + bias_i       rounded once to x's type
+// the shift, centring and correction of the variance in sv_lib.hip: a row of
+// equal values has d = 0 exactly, and a mean far from zero cancels before
+// anything is squared.
+//
+// Backward, with the mean and rstd the forward pass wrote, d_i = x_i - mean,
+// b = sum(d) / n (what the float32 mean is off by), g_i = dy_i * w_i:
+//   xhat_i = (d_i - b) * rstd
+//   dx_i = rstd * ((g_i - sum(g) / n) - xhat_i * c),
+//          c = rstd * (sum(g d) - b * sum(g)) / n  ( = sum(g xhat) / n )
+//   dw_j = sum over rows of dy * xhat,  dbias_j = sum over rows of dy.
+//
+// Every sum has one fixed order given by the shape and the type, so results
+// are the same bits from run to run, and a row's y and dx do not depend on
+// the other rows.
+#include "sv_rows.hpp"
+
+using svh::check_device;
+using svh::check_launch;
+using svh::fail;
+using svh::ok;
+using svr::Node;
+
+namespace {
+
+constexpr int ROW_THREADS = 256;
+constexpr int64_t ROW_GRID = 8192;     // workgroups of a row launch, at most
+constexpr int COL_ROWS = 64;           // rows of one partial column sum
+constexpr int64_t COL_MAX_GROUPS = 512;
+
+// 1 / sqrt(v) in double (one Newton step from the hardware's estimate, about
+// 2^-46), so that the float32 value is the rounded one; 0, Inf and NaN as
+// the estimate gives them.
+__device__ __forceinline__ float rstd_of(float var, double eps) {
+  const double v = (double)var + eps;
+  const double r = __builtin_amdgcn_rsq(v);
+  const double e = 1.0 - v * r * r;
+  const double s = r + 0.5 * r * e;
+  return (float)(__builtin_isfinite(e) ? s : r);
+}
+
+// Sum of one node per thread over the workgroup, in a fixed order; every
+// thread gets the root's value.  `lds` holds a node per wave.
+template <int WAVES>
+__device__ __forceinline__ float block_sum(Node n, Node *lds) {
+  n = sv::wave_tree<sv::NODE_TWOSUM>(n);
+  if constexpr (WAVES > 1) {
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = n;
+    __syncthreads();
+    Node w[WAVES];
+#pragma unroll
+    for (int i = 0; i < WAVES; ++i) w[i] = lds[i];
+    n = sv::node_tree<0, WAVES, WAVES>(w);
+  }
+  return sv::root_value(n);
+}
+
+// Rows of any length: a workgroup per row, each pass reads the row again.
+// Compensated sums, as a thread adds up a long run of values one by one.
+template <class T>
+__global__ __launch_bounds__(ROW_THREADS) void k_norm_any(const T *__restrict__ x, int64_t rows, int n, int64_t ldx,
+                                                          const void *__restrict__ w, const void *__restrict__ bias,
+                                                          int pt, double eps, T *__restrict__ y, int64_t ldy,
+                                                          float *__restrict__ mean, float *__restrict__ rstd) {
+  __shared__ Node lds[ROW_THREADS / 64];
+  for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
+    const T *xr = x + r * ldx;
+    const float fn = (float)n;
+    const float x0 = n > 0 ? svr::to_f(xr[0]) : 0.0f;
+    Node a = sv::zero_node();
+    for (int i = threadIdx.x; i < n; i += ROW_THREADS) svr::add_to(a, svr::to_f(xr[i]) - x0);
+    const float m1 = x0 + block_sum<ROW_THREADS / 64>(a, lds) / fn;
+    Node s1 = sv::zero_node(), s2 = sv::zero_node();
+    for (int i = threadIdx.x; i < n; i += ROW_THREADS) {
+      const float d = svr::to_f(xr[i]) - m1;
+      svr::add_to(s1, d);
+      svr::add_to(s2, d * d);
+    }
+    const float b = block_sum<ROW_THREADS / 64>(s1, lds) / fn;
+    const float q = block_sum<ROW_THREADS / 64>(s2, lds) / fn - b * b;
+    const float var = q <= 0.0f ? 0.0f : q;  // a NaN stays
+    const float rs = rstd_of(var, eps);
+    if (threadIdx.x == 0) {
+      if (mean) mean[r] = m1 + b;
+      if (rstd) rstd[r] = rs;
+    }
+    T *yr = y + r * ldy;
+    for (int i = threadIdx.x; i < n; i += ROW_THREADS) {
+      float v = ((svr::to_f(xr[i]) - m1) - b) * rs;
+      if (w) v = v * svr::load_as(w, i, pt);
+      if (bias) v = v + svr::load_as(bias, i, pt);
+      yr[i] = svr::from_f<T>(v);
+    }
+  }
+}
+
+// The rows' part of the backward pass: dx and, for the column sums, b.
+template <class T>
+__global__ __launch_bounds__(ROW_THREADS) void k_norm_dx_any(
+    const T *__restrict__ dy, int64_t lddy, const T *__restrict__ x, int64_t ldx, int64_t rows, int n,
+    const void *__restrict__ w, int pt, const float *__restrict__ mean, const float *__restrict__ rstd,
+    T *__restrict__ dx, int64_t lddx, float *__restrict__ off) {
+  __shared__ Node lds[ROW_THREADS / 64];
+  for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
+    const T *xr = x + r * ldx, *gr = dy + r * lddy;
+    const float fn = (float)n, m = mean[r], rs = rstd[r];
+    Node sd = sv::zero_node(), sg = sv::zero_node(), sgd = sv::zero_node();
+    for (int i = threadIdx.x; i < n; i += ROW_THREADS) {
+      const float d = svr::to_f(xr[i]) - m;
+      const float g = w ? svr::to_f(gr[i]) * svr::load_as(w, i, pt) : svr::to_f(gr[i]);
+      svr::add_to(sd, d);
+      svr::add_to(sg, g);
+      svr::add_to(sgd, g * d);
+    }
+    const float b = block_sum<ROW_THREADS / 64>(sd, lds) / fn;
+    const float sumg = block_sum<ROW_THREADS / 64>(sg, lds);
+    const float sumgd = block_sum<ROW_THREADS / 64>(sgd, lds);
+    const float a = sumg / fn;
+    const float c = rs * ((sumgd - b * sumg) / fn);
+    if (off && threadIdx.x == 0) off[r] = b;
+    if (dx) {
+      T *dr = dx + r * lddx;
+      for (int i = threadIdx.x; i < n; i += ROW_THREADS) {
+        const float xh = ((svr::to_f(xr[i]) - m) - b) * rs;
+        const float g = w ? svr::to_f(gr[i]) * svr::load_as(w, i, pt) : svr::to_f(gr[i]);
+        dr[i] = svr::from_f<T>(rs * ((g - a) - xh * c));
+      }
+    }
+  }
+}
+
+// The columns' part: group q of the rows (row r belongs to group r mod
+// groups) and 64 columns per workgroup; each wave takes every fourth row of the group.
+template <class T>
+__global__ __launch_bounds__(256) void k_norm_dw_any(const T *__restrict__ dy, int64_t lddy, const T *__restrict__ x,
+                                                     int64_t ldx, int64_t rows, int n, const float *__restrict__ mean,
+                                                     const float *__restrict__ rstd, const float *__restrict__ off,
+                                                     int groups, int ctiles, Node *__restrict__ part) {
+  __shared__ Node lds[2][4][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int q = blockIdx.x / ctiles, j = (blockIdx.x % ctiles) * 64 + lane;
+  Node dw = sv::zero_node(), db = sv::zero_node();
+  if (j < n) {
+    for (int64_t r = q + (int64_t)wave * groups; r < rows; r += 4 * (int64_t)groups) {
+      const float g = svr::to_f(dy[r * lddy + j]);
+      const float xh = ((svr::to_f(x[r * ldx + j]) - mean[r]) - off[r]) * rstd[r];
+      svr::add_to(dw, g * xh);
+      svr::add_to(db, g);
+    }
+  }
+  lds[0][wave][lane] = dw;
+  lds[1][wave][lane] = db;
+  __syncthreads();
+  if (wave < 2 && j < n) {
+    Node t[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) t[i] = lds[wave][i][lane];
+    part[((int64_t)q * 2 + wave) * n + j] = sv::node_tree<0, 4, 4>(t);
+  }
+}
+
+// Joins the groups' partial sums of 64 columns of dw (blocks [0, ctiles)) or
+// dbias (blocks [ctiles, 2 ctiles)), in group order.
+__global__ __launch_bounds__(256) void k_norm_join(const Node *__restrict__ part, int groups, int n, int ctiles,
+                                                   void *__restrict__ dw, void *__restrict__ db, int pt) {
+  __shared__ Node lds[4][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int which = blockIdx.x / ctiles, j = (blockIdx.x % ctiles) * 64 + lane;
+  Node s = sv::zero_node();
+  if (j < n)
+    for (int q = wave; q < groups; q += 4) s = sv::combine(s, part[((int64_t)q * 2 + which) * n + j]);
+  lds[wave][lane] = s;
+  __syncthreads();
+  void *out = which ? db : dw;
+  if (wave == 0 && j < n && out) {
+    Node t[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) t[i] = lds[i][lane];
+    svr::store_as(out, j, pt, sv::root_value(sv::node_tree<0, 4, 4>(t)));
+  }
+}
+
+// Groups of rows: 64 rows each or more, at most 512 and at most 2^22
+// workgroups in all (2^30 work-items, within HIP's grid limit).
+int64_t col_groups(int64_t rows, int64_t n) {
+  const int64_t ctiles = (n + 63) / 64;
+  int64_t g = (rows + COL_ROWS - 1) / COL_ROWS;
+  if (g > COL_MAX_GROUPS) g = COL_MAX_GROUPS;
+  if (g > ((int64_t)1 << 22) / ctiles) g = ((int64_t)1 << 22) / ctiles;
+  return g < 1 ? 1 : g;
+}
+
+// Checks that the two calls share; SV_OK without touching the message.
+sv_status check_rows(const char *who, int dtype, int64_t rows, int64_t n, int param_dtype) {
+  if (!svr::dtype_bytes(dtype)) return fail(SV_ERR_INVALID_ARGUMENT, "%s: dtype %d is not a type code", who, dtype);
+  if (param_dtype != dtype && param_dtype != SV_DTYPE_F32)
+    return fail(SV_ERR_INVALID_ARGUMENT, "%s: param_dtype %d must be the rows' type or SV_DTYPE_F32", who,
+                param_dtype);
+  if (rows < 0 || n < 0)
+    return fail(SV_ERR_INVALID_ARGUMENT, "%s: rows = %lld, n = %lld must be >= 0", who, (long long)rows,
+                (long long)n);
+  if (n > svr::MAX_N) return fail(SV_ERR_UNSUPPORTED, "%s: rows of %lld values exceed 2^27", who, (long long)n);
+  if (n > 0 && rows > svr::MAX_VALUES / n)
+    return fail(SV_ERR_UNSUPPORTED, "%s: %lld x %lld values exceed 2^36", who, (long long)rows, (long long)n);
+  if (rows > svr::MAX_VALUES)
+    return fail(SV_ERR_UNSUPPORTED, "%s: %lld rows exceed 2^36", who, (long long)rows);
+  return SV_OK;
+}
+
+unsigned row_grid(int64_t rows) { return (unsigned)(rows < ROW_GRID ? rows : ROW_GRID); }
+
+}  // namespace
+
+extern "C" {
+
+sv_status sv_layer_norm(const void *x, int dtype, int64_t rows, int64_t n, int64_t ldx, const void *weight,
+                        const void *bias, int param_dtype, double eps, void *y, int64_t ldy, float *mean, float *rstd,
+                        void *stream) {
+  static const char who[] = "sv_layer_norm";
+  sv_status st = check_rows(who, dtype, rows, n, param_dtype);
+  if (st != SV_OK) return st;
+  if (!(eps >= 0.0) || eps > 3.0e38) return fail(SV_ERR_INVALID_ARGUMENT, "%s: eps must be >= 0 and finite", who);
+  const size_t e = svr::dtype_bytes(dtype);
+  if ((st = svr::check_matrix(who, "x", x, ldx, rows, n, e)) != SV_OK) return st;
+  if ((st = svr::check_matrix(who, "y", y, ldy, rows, n, e)) != SV_OK) return st;
+  const size_t pe = svr::dtype_bytes(param_dtype);
+  if (weight && (st = svr::check_matrix(who, "weight", weight, n, 1, n, pe)) != SV_OK) return st;
+  if (bias && (st = svr::check_matrix(who, "bias", bias, n, 1, n, pe)) != SV_OK) return st;
+  if (rows == 0) return ok();
+  if ((st = check_device()) != SV_OK) return st;
+  (void)hipGetLastError();
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  svr::with_type(dtype, [&](auto t) {
+    using T = decltype(t);
+    k_norm_any<T><<<row_grid(rows), ROW_THREADS, 0, s>>>((const T *)x, rows, (int)n, ldx, weight, bias, param_dtype,
+                                                         eps, (T *)y, ldy, mean, rstd);
+  });
+  return check_launch(who);
+}
+
+size_t sv_layer_norm_backward_workspace_size(int64_t rows, int64_t n, int dtype) {
+  if (!svr::dtype_bytes(dtype) || rows < 0 || n < 0 || n > svr::MAX_N || rows > svr::MAX_VALUES ||
+      (n > 0 && rows > svr::MAX_VALUES / n))
+    return (size_t)-1;
+  if (n == 0) return 0;
+  return svr::round256((size_t)rows * 4) + (size_t)col_groups(rows, n) * 2 * (size_t)n * sizeof(Node);
+}
+
+sv_status sv_layer_norm_backward(const void *dy, int64_t lddy, const void *x, int64_t ldx, int dtype, int64_t rows,
+                                 int64_t n, const void *weight, int param_dtype, const float *mean, const float *rstd,
+                                 void *dx, int64_t lddx, void *dweight, void *dbias, void *workspace,
+                                 size_t workspace_bytes, void *stream) {
+  static const char who[] = "sv_layer_norm_backward";
+  sv_status st = check_rows(who, dtype, rows, n, param_dtype);
+  if (st != SV_OK) return st;
+  const size_t e = svr::dtype_bytes(dtype);
+  if ((st = svr::check_matrix(who, "dy", dy, lddy, rows, n, e)) != SV_OK) return st;
+  if ((st = svr::check_matrix(who, "x", x, ldx, rows, n, e)) != SV_OK) return st;
+  const size_t pe = svr::dtype_bytes(param_dtype);
+  if (weight && (st = svr::check_matrix(who, "weight", weight, n, 1, n, pe)) != SV_OK) return st;
+  if (dweight && (st = svr::check_matrix(who, "dweight", dweight, n, 1, n, pe)) != SV_OK) return st;
+  if (dbias && (st = svr::check_matrix(who, "dbias", dbias, n, 1, n, pe)) != SV_OK) return st;
+  if (dx && (st = svr::check_matrix(who, "dx", dx, lddx, rows, n, e)) != SV_OK) return st;
+  if (rows > 0 && n > 0 && (!mean || !rstd))
+    return fail(SV_ERR_INVALID_ARGUMENT, "%s: mean or rstd is NULL", who);
+  if (n == 0 || (!dx && !dweight && !dbias)) return ok();
+  const bool cols = dweight || dbias;
+  if (!cols && rows == 0) return ok();
+  const size_t need = sv_layer_norm_backward_workspace_size(rows, n, dtype);
+  if (cols) {
+    if (!workspace) return fail(SV_ERR_WORKSPACE, "%s: workspace is NULL (%zu bytes needed)", who, need);
+    if (workspace_bytes < need)
+      return fail(SV_ERR_WORKSPACE, "%s: workspace has %zu bytes, %zu needed", who, workspace_bytes, need);
+    if (!svh::aligned256(workspace)) return fail(SV_ERR_WORKSPACE, "%s: workspace is not 256-byte aligned", who);
+  }
+  if ((st = check_device()) != SV_OK) return st;
+  (void)hipGetLastError();
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  float *off = cols ? reinterpret_cast<float *>(workspace) : nullptr;
+  Node *part = cols ? reinterpret_cast<Node *>((char *)workspace + svr::round256((size_t)rows * 4)) : nullptr;
+  const int groups = (int)col_groups(rows, n), ctiles = (int)((n + 63) / 64);
+  svr::with_type(dtype, [&](auto t) {
+    using T = decltype(t);
+    const T *g = (const T *)dy, *xx = (const T *)x;
+    if (rows > 0)
+      k_norm_dx_any<T><<<row_grid(rows), ROW_THREADS, 0, s>>>(g, lddy, xx, ldx, rows, (int)n, weight, param_dtype,
+                                                              mean, rstd, (T *)dx, lddx, off);
+    if (cols)
+      k_norm_dw_any<T><<<(unsigned)(groups * ctiles), 256, 0, s>>>(g, lddy, xx, ldx, rows, (int)n, mean, rstd, off,
+                                                                   groups, ctiles, part);
+  });
+  if (cols)
+    k_norm_join<<<(unsigned)(2 * ctiles), 256, 0, s>>>(part, groups, (int)n, ctiles, dweight, dbias, param_dtype);
+  return check_launch(who);
+}
+
+}  // extern "C"
