@@ -64,6 +64,111 @@ __device__ __forceinline__ float block_sum(Node n, Node *lds) {
   return sv::root_value(n);
 }
 
+// Rows that a group of L threads holds in registers, K chunks of 16 bytes per
+// thread: the row is read once, and the group's R - 1 neighbours in the
+// workgroup hold other rows.  The next row's loads are in flight while a row
+// is summed (PRE), and the parameters stay in registers across rows (WREG).
+// Plain pairwise sums: with the shift and the second centring each is a sum
+// of values of the size of the spread, and 12 levels of rounding stay below
+// the result's own.
+template <class T, int L, int K, bool FULL>
+__global__ __launch_bounds__(L < 256 ? 256 : L) void k_norm_rows(
+    const T *__restrict__ x, int64_t rows, int n, int64_t ldx, const void *__restrict__ w,
+    const void *__restrict__ bias, int pt, double eps, T *__restrict__ y, int64_t ldy, float *__restrict__ mean,
+    float *__restrict__ rstd) {
+  using Tile = svr::RowTile<T, L, K, FULL>;
+  constexpr int E = Tile::E, TPB = L < 256 ? 256 : L, R = TPB / L;
+  constexpr bool HOLD = E <= 16;
+  __shared__ float lds_a[TPB / 64], lds_b[2 * TPB / 64];
+  const int g = threadIdx.x / L, l0 = threadIdx.x % L;
+  const float inv_n = 1.0f / (float)n;
+  constexpr int VE = Tile::VE;
+  float wv[HOLD ? E : 1], bv[HOLD ? E : 1];
+  if constexpr (HOLD) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      svr::load_param<T, L>(w, pt, n, l0, k, 1.0f, wv + k * VE);
+      svr::load_param<T, L>(bias, pt, n, l0, k, 0.0f, bv + k * VE);
+    }
+  }
+  const int64_t step = (int64_t)gridDim.x * R;
+  typename Tile::Vec raw[K];
+  T first{};
+  const bool wide = n >= Tile::VE;
+  int64_t r = (int64_t)blockIdx.x * R + g;
+  if (r < rows) {
+    Tile::load(x + r * ldx, n, l0, wide && r + 1 < rows, raw);
+    first = x[r * ldx];
+  }
+  for (int64_t r0 = (int64_t)blockIdx.x * R; r0 < rows; r0 += step, r += step) {
+    int l = l0;  // opaque, so that the addresses of all chunks are not kept in registers across rows
+    asm volatile("" : "+v"(l));
+    float f[E];
+    Tile::unpack(raw, f);
+    const float x0 = svr::to_f(first);
+    if (HOLD && r + step < rows) {
+      Tile::load(x + (r + step) * ldx, n, l, wide && r + step + 1 < rows, raw);
+      first = x[(r + step) * ldx];
+    }
+    float a[1] = {svr::pair_sum<0, E>([&](int i) { return Tile::inside(n, l, i) ? f[i] - x0 : 0.0f; })};
+    svr::group_sum<L, 1>(a, lds_a);
+    const float m1 = x0 + a[0] * inv_n;
+#pragma unroll
+    for (int i = 0; i < E; ++i) f[i] = Tile::inside(n, l, i) ? f[i] - m1 : 0.0f;
+    float s[2] = {svr::pair_sum<0, E>([&](int i) { return f[i]; }),
+                  svr::pair_sum<0, E>([&](int i) { return f[i] * f[i]; })};
+    svr::group_sum<L, 2>(s, lds_b);
+    const float b = s[0] * inv_n;
+    const float q = s[1] * inv_n - b * b;
+    const float rs = rstd_of(q <= 0.0f ? 0.0f : q, eps);  // a NaN stays
+    if (r < rows) {
+      if (l == 0) {
+        if (mean) mean[r] = m1 + b;
+        if (rstd) rstd[r] = rs;
+      }
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        float wk[VE], bk[VE];
+        if constexpr (!HOLD) {
+          svr::load_param<T, L>(w, pt, n, l, k, 1.0f, wk);
+          svr::load_param<T, L>(bias, pt, n, l, k, 0.0f, bk);
+        }
+#pragma unroll
+        for (int i = 0; i < VE; ++i) {
+          const float ww = HOLD ? wv[HOLD ? k * VE + i : 0] : wk[i], bb = HOLD ? bv[HOLD ? k * VE + i : 0] : bk[i];
+          f[k * VE + i] = ((f[k * VE + i] - b) * rs) * ww + bb;
+        }
+        Tile::store_chunk(y + r * ldy, n, l, k, f);
+        if constexpr (!HOLD) __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+    if (!HOLD && r + step < rows) {
+      Tile::load(x + (r + step) * ldx, n, l, wide && r + step + 1 < rows, raw);
+      first = x[(r + step) * ldx];
+    }
+  }
+}
+
+// Calls fn(L, K) (integral constants) with the smallest tile that holds n
+// values of T; false when none does.
+template <class T, class Fn>
+bool with_tile(int64_t n, Fn &&fn) {
+  constexpr int VE = svr::Chunk<T>::VE;
+#define SV_TILE(L, K)                                                              \
+  if (n <= (int64_t)(L) * (K)*VE) {                                                \
+    fn(std::integral_constant<int, L>{}, std::integral_constant<int, K>{});        \
+    return true;                                                                   \
+  }
+  SV_TILE(1, 1) SV_TILE(2, 1) SV_TILE(4, 1) SV_TILE(8, 1) SV_TILE(16, 1) SV_TILE(32, 1) SV_TILE(64, 1) SV_TILE(64, 2)
+  if constexpr (VE == 8) {
+    SV_TILE(128, 2) SV_TILE(256, 2) SV_TILE(512, 2) SV_TILE(1024, 2) SV_TILE(1024, 4)
+  } else {
+    SV_TILE(64, 4) SV_TILE(128, 4) SV_TILE(256, 4) SV_TILE(512, 4) SV_TILE(1024, 4) SV_TILE(1024, 8)
+  }
+#undef SV_TILE
+  return false;
+}
+
 // Rows of any length: a workgroup per row, each pass reads the row again.
 // Compensated sums, as a thread adds up a long run of values one by one.
 template <class T>
@@ -241,6 +346,15 @@ sv_status sv_layer_norm(const void *x, int dtype, int64_t rows, int64_t n, int64
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   svr::with_type(dtype, [&](auto t) {
     using T = decltype(t);
+    // an empty row has no first value to shift by (x may be NULL)
+    const bool held = n > 0 && with_tile<T>(n, [&](auto tl, auto tk) {
+      constexpr int L = decltype(tl)::value, K = decltype(tk)::value, TPB = L < 256 ? 256 : L, R = TPB / L;
+      const int64_t blocks = (rows + R - 1) / R, most = 256 * (2048 / TPB);
+      auto *k = n == (int64_t)L * K * svr::Chunk<T>::VE ? k_norm_rows<T, L, K, true> : k_norm_rows<T, L, K, false>;
+      k<<<(unsigned)(blocks < most ? blocks : most), TPB, 0, s>>>((const T *)x, rows, (int)n, ldx, weight, bias,
+                                                                  param_dtype, eps, (T *)y, ldy, mean, rstd);
+    });
+    if (held) return;
     k_norm_any<T><<<row_grid(rows), ROW_THREADS, 0, s>>>((const T *)x, rows, (int)n, ldx, weight, bias, param_dtype,
                                                          eps, (T *)y, ldy, mean, rstd);
   });

@@ -5,6 +5,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "../../include/stable_variance.h"
 #include "sv_device.hpp"
 #include "sv_host.hpp"
@@ -23,7 +25,7 @@ __device__ __forceinline__ float to_f(T v) { return (float)v; }
 // of the places that must agree and not in others.
 template <class T>
 __device__ __forceinline__ T from_f(float v) {
-  if constexpr (sizeof(T) == 2) asm("" : "+v"(v));
+  if constexpr (std::is_same_v<T, f16>) asm("" : "+v"(v));
   return (T)v;
 }
 
@@ -38,6 +40,135 @@ __device__ __forceinline__ void store_as(void *p, int64_t i, int dtype, float v)
   if (dtype == SV_DTYPE_BF16) reinterpret_cast<bf16 *>(p)[i] = from_f<bf16>(v);
   else if (dtype == SV_DTYPE_F16) reinterpret_cast<f16 *>(p)[i] = from_f<f16>(v);
   else reinterpret_cast<float *>(p)[i] = v;
+}
+
+// ---------------------------------------------------------------- 16-byte chunks
+
+// VE values in one 16-byte load or store.  The address needs the alignment
+// of T only: global memory takes 16-byte accesses at any address.
+template <class T>
+struct Chunk {
+  static constexpr int VE = 16 / (int)sizeof(T);
+  typedef T Vec __attribute__((ext_vector_type(VE)));
+  Vec v;
+};
+
+// A row of n values held by L threads, K chunks each: thread l's chunk k
+// starts at value (k * L + l) * VE.  FULL: n == K * L * VE.
+template <class T, int L, int K, bool FULL>
+struct RowTile {
+  static constexpr int VE = Chunk<T>::VE, E = K * VE;
+  using Vec = typename Chunk<T>::Vec;
+
+  // Loads the row.  Values past n hold anything.  `over`: the VE - 1 values
+  // behind the row may be read (a further row of at least VE values follows),
+  // so that its last chunk takes one load like the others.
+  __device__ static __forceinline__ void load(const T *__restrict__ p, int n, int l, bool over, Vec (&raw)[K]) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int e = (k * L + l) * VE;
+      if (FULL || e + VE <= n || (over && e < n)) {
+        __builtin_memcpy(&raw[k], p + e, 16);
+      } else if (e < n) {
+#pragma unroll
+        for (int i = 0; i < VE - 1; ++i)
+          if (e + i < n) raw[k][i] = p[e + i];
+      }
+    }
+  }
+
+  __device__ static __forceinline__ void unpack(const Vec (&raw)[K], float (&f)[E]) {
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+      for (int i = 0; i < VE; ++i) f[k * VE + i] = to_f<T>(raw[k][i]);
+  }
+
+  // Value i of thread l lies inside the row.
+  __device__ static __forceinline__ bool inside(int n, int l, int i) {
+    return FULL || ((i / VE) * L + l) * VE + i % VE < n;
+  }
+
+  // Chunk k of the row's values f.
+  __device__ static __forceinline__ void store_chunk(T *__restrict__ p, int n, int l, int k, const float (&f)[E]) {
+    const int e = (k * L + l) * VE;
+    Vec v;
+#pragma unroll
+    for (int i = 0; i < VE; ++i) v[i] = from_f<T>(f[k * VE + i]);
+    if (FULL || e + VE <= n) {
+      __builtin_memcpy(p + e, &v, 16);
+    } else if (e < n) {
+#pragma unroll
+      for (int i = 0; i < VE - 1; ++i)
+        if (e + i < n) p[e + i] = v[i];
+    }
+  }
+};
+
+// Chunk k of thread l of a parameter vector whose type is a launch argument:
+// VE values from e = (k * L + l) * VE on, `none` past n and for p == nullptr.
+template <class T, int L>
+__device__ __forceinline__ void load_param(const void *__restrict__ p, int dtype, int n, int l, int k, float none,
+                                           float *__restrict__ out) {
+  constexpr int VE = Chunk<T>::VE;
+  const int e = (k * L + l) * VE;
+#pragma unroll
+  for (int i = 0; i < VE; ++i) out[i] = none;
+  if (!p) return;
+  if (e + VE <= n) {
+    if (sizeof(T) == 2 && dtype != SV_DTYPE_F32) {
+      typename Chunk<T>::Vec v;
+      __builtin_memcpy(&v, reinterpret_cast<const T *>(p) + e, 16);
+#pragma unroll
+      for (int i = 0; i < VE; ++i) out[i] = to_f<T>(v[i]);
+    } else {
+      float v[VE];
+      __builtin_memcpy(v, reinterpret_cast<const float *>(p) + e, 4 * VE);
+#pragma unroll
+      for (int i = 0; i < VE; ++i) out[i] = v[i];
+    }
+  } else if (e < n) {
+#pragma unroll
+    for (int i = 0; i < VE - 1; ++i)
+      if (e + i < n) out[i] = load_as(p, e + i, dtype);
+  }
+}
+
+// Pairwise sum of N values fn(OFF), fn(OFF + 1), .. (adjacent pairs at each
+// level).
+template <int OFF, int N, class Fn>
+__device__ __forceinline__ float pair_sum(Fn &&fn) {
+  if constexpr (N == 1) return fn(OFF);
+  else return pair_sum<OFF, N / 2>(fn) + pair_sum<OFF + N / 2, N / 2>(fn);
+}
+
+// Sums of NV values per thread over each group of L consecutive threads, in
+// a fixed order (lanes pairwise, then the group's waves pairwise); every
+// thread of the group gets them.  L > 64 takes a barrier and `lds`, which
+// holds NV floats per wave of the workgroup; the next use of the same `lds`
+// must lie behind another barrier.
+template <int L, int NV>
+__device__ __forceinline__ void group_sum(float (&v)[NV], float *lds) {
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+    v[i] = sv::seg_tree<sv::NODE_PLAIN, (L < 64 ? L : 64)>(Node{v[i], 0.0f}).s;
+  if constexpr (L > 64) {
+    constexpr int W = L / 64;
+    const int wave = threadIdx.x >> 6;
+    if ((threadIdx.x & 63) == 0) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) lds[wave * NV + i] = v[i];
+    }
+    __syncthreads();
+    const float *g = lds + (wave & ~(W - 1)) * NV;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      float t[W];
+#pragma unroll
+      for (int j = 0; j < W; ++j) t[j] = g[j * NV + i];
+      v[i] = pair_sum<0, W>([&](int j) { return t[j]; });
+    }
+  }
 }
 
 // One more value for a compensated sum: TwoSum, the error added to the carry.
