@@ -64,6 +64,9 @@ __device__ __forceinline__ float block_sum(Node n, Node *lds) {
   return sv::root_value(n);
 }
 
+// Threads of a workgroup whose groups of L threads hold a row each.
+constexpr int tpb(int L) { return L <= 128 ? 256 : L; }
+
 // Rows that a group of L threads holds in registers, K chunks of 16 bytes per
 // thread: the row is read once, and the group's R - 1 neighbours in the
 // workgroup hold other rows.  The next row's loads are in flight while a row
@@ -72,12 +75,12 @@ __device__ __forceinline__ float block_sum(Node n, Node *lds) {
 // of values of the size of the spread, and 12 levels of rounding stay below
 // the result's own.
 template <class T, int L, int K, bool FULL>
-__global__ __launch_bounds__(L < 256 ? 256 : L) void k_norm_rows(
+__global__ __launch_bounds__(tpb(L)) void k_norm_rows(
     const T *__restrict__ x, int64_t rows, int n, int64_t ldx, const void *__restrict__ w,
     const void *__restrict__ bias, int pt, double eps, T *__restrict__ y, int64_t ldy, float *__restrict__ mean,
     float *__restrict__ rstd) {
   using Tile = svr::RowTile<T, L, K, FULL>;
-  constexpr int E = Tile::E, TPB = L < 256 ? 256 : L, R = TPB / L;
+  constexpr int E = Tile::E, TPB = tpb(L), R = TPB / L;
   constexpr bool HOLD = E <= 16;
   __shared__ float lds_a[TPB / 64], lds_b[2 * TPB / 64];
   const int g = threadIdx.x / L, l0 = threadIdx.x % L;
@@ -94,10 +97,9 @@ __global__ __launch_bounds__(L < 256 ? 256 : L) void k_norm_rows(
   const int64_t step = (int64_t)gridDim.x * R;
   typename Tile::Vec raw[K];
   T first{};
-  const bool wide = n >= Tile::VE;
   int64_t r = (int64_t)blockIdx.x * R + g;
   if (r < rows) {
-    Tile::load(x + r * ldx, n, l0, wide && r + 1 < rows, raw);
+    Tile::load(x + r * ldx, n, Tile::avail(rows, r, ldx, n), l0, raw);
     first = x[r * ldx];
   }
   for (int64_t r0 = (int64_t)blockIdx.x * R; r0 < rows; r0 += step, r += step) {
@@ -105,9 +107,10 @@ __global__ __launch_bounds__(L < 256 ? 256 : L) void k_norm_rows(
     asm volatile("" : "+v"(l));
     float f[E];
     Tile::unpack(raw, f);
+    if (r < rows) Tile::load_rest(x + r * ldx, n, Tile::avail(rows, r, ldx, n), l, f);
     const float x0 = svr::to_f(first);
     if (HOLD && r + step < rows) {
-      Tile::load(x + (r + step) * ldx, n, l, wide && r + step + 1 < rows, raw);
+      Tile::load(x + (r + step) * ldx, n, Tile::avail(rows, r + step, ldx, n), l, raw);
       first = x[(r + step) * ldx];
     }
     float a[1] = {svr::pair_sum<0, E>([&](int i) { return Tile::inside(n, l, i) ? f[i] - x0 : 0.0f; })};
@@ -143,7 +146,7 @@ __global__ __launch_bounds__(L < 256 ? 256 : L) void k_norm_rows(
       }
     }
     if (!HOLD && r + step < rows) {
-      Tile::load(x + (r + step) * ldx, n, l, wide && r + step + 1 < rows, raw);
+      Tile::load(x + (r + step) * ldx, n, Tile::avail(rows, r + step, ldx, n), l, raw);
       first = x[(r + step) * ldx];
     }
   }
@@ -159,12 +162,14 @@ bool with_tile(int64_t n, Fn &&fn) {
     fn(std::integral_constant<int, L>{}, std::integral_constant<int, K>{});        \
     return true;                                                                   \
   }
-  SV_TILE(1, 1) SV_TILE(2, 1) SV_TILE(4, 1) SV_TILE(8, 1) SV_TILE(16, 1) SV_TILE(32, 1) SV_TILE(64, 1) SV_TILE(64, 2)
-  if constexpr (VE == 8) {
-    SV_TILE(128, 2) SV_TILE(256, 2) SV_TILE(512, 2) SV_TILE(1024, 2) SV_TILE(1024, 4)
-  } else {
-    SV_TILE(64, 4) SV_TILE(128, 4) SV_TILE(256, 4) SV_TILE(512, 4) SV_TILE(1024, 4) SV_TILE(1024, 8)
-  }
+  // up to 64 lanes with one chunk each, then whole waves with 16 values per
+  // thread, then 32 (the parameters are then read again for every row)
+  SV_TILE(1, 1) SV_TILE(2, 1) SV_TILE(4, 1) SV_TILE(8, 1) SV_TILE(16, 1) SV_TILE(32, 1) SV_TILE(64, 1)
+  if constexpr (VE == 4) { SV_TILE(64, 2) }
+  constexpr int KH = 16 / VE;
+  SV_TILE(64, KH) SV_TILE(128, KH) SV_TILE(192, KH) SV_TILE(256, KH) SV_TILE(320, KH) SV_TILE(384, KH)
+  SV_TILE(448, KH) SV_TILE(512, KH) SV_TILE(640, KH) SV_TILE(768, KH) SV_TILE(896, KH) SV_TILE(1024, KH)
+  SV_TILE(1024, 2 * KH)
 #undef SV_TILE
   return false;
 }
@@ -348,7 +353,7 @@ sv_status sv_layer_norm(const void *x, int dtype, int64_t rows, int64_t n, int64
     using T = decltype(t);
     // an empty row has no first value to shift by (x may be NULL)
     const bool held = n > 0 && with_tile<T>(n, [&](auto tl, auto tk) {
-      constexpr int L = decltype(tl)::value, K = decltype(tk)::value, TPB = L < 256 ? 256 : L, R = TPB / L;
+      constexpr int L = decltype(tl)::value, K = decltype(tk)::value, TPB = tpb(L), R = TPB / L;
       const int64_t blocks = (rows + R - 1) / R, most = 256 * (2048 / TPB);
       auto *k = n == (int64_t)L * K * svr::Chunk<T>::VE ? k_norm_rows<T, L, K, true> : k_norm_rows<T, L, K, false>;
       k<<<(unsigned)(blocks < most ? blocks : most), TPB, 0, s>>>((const T *)x, rows, (int)n, ldx, weight, bias,

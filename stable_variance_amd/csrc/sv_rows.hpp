@@ -60,19 +60,37 @@ struct RowTile {
   static constexpr int VE = Chunk<T>::VE, E = K * VE;
   using Vec = typename Chunk<T>::Vec;
 
-  // Loads the row.  Values past n hold anything.  `over`: the VE - 1 values
-  // behind the row may be read (a further row of at least VE values follows),
-  // so that its last chunk takes one load like the others.
-  __device__ static __forceinline__ void load(const T *__restrict__ p, int n, int l, bool over, Vec (&raw)[K]) {
+  // Values that may be read from the start of row r on (the rest of the
+  // matrix, at least n), as far as a tile needs it.
+  __device__ static __forceinline__ int avail(int64_t rows, int64_t r, int64_t ld, int n) {
+    const int64_t a = (rows - 1 - r) * ld + n;
+    return a < (1 << 24) ? (int)a : (1 << 24);
+  }
+
+  // Starts the loads of the row; values past n hold anything.  The row's last
+  // chunk may reach into the next row.  Where there is none it is left out
+  // (load_rest brings it): a second way to write the same registers would
+  // make the compiler wait for the loads here.
+  __device__ static __forceinline__ void load(const T *__restrict__ p, int n, int avail, int l, Vec (&raw)[K]) {
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       const int e = (k * L + l) * VE;
-      if (FULL || e + VE <= n || (over && e < n)) {
-        __builtin_memcpy(&raw[k], p + e, 16);
-      } else if (e < n) {
+      if (FULL || (e < n && e + VE <= avail)) __builtin_memcpy(&raw[k], p + e, 16);
+    }
+  }
+
+  // The values of the last chunks that load left out.
+  __device__ static __forceinline__ void load_rest(const T *__restrict__ p, int n, int avail, int l, float (&f)[E]) {
+    if constexpr (!FULL) {
+      if (((n + VE - 1) & -VE) <= avail) return;  // the same for all lanes of a row
 #pragma unroll
-        for (int i = 0; i < VE - 1; ++i)
-          if (e + i < n) raw[k][i] = p[e + i];
+      for (int k = 0; k < K; ++k) {
+        const int e = (k * L + l) * VE;
+        if (e < n && e + VE > avail) {
+#pragma unroll
+          for (int i = 0; i < VE - 1; ++i)
+            if (e + i < n) f[k * VE + i] = to_f<T>(p[e + i]);
+        }
       }
     }
   }
@@ -139,7 +157,7 @@ __device__ __forceinline__ void load_param(const void *__restrict__ p, int dtype
 template <int OFF, int N, class Fn>
 __device__ __forceinline__ float pair_sum(Fn &&fn) {
   if constexpr (N == 1) return fn(OFF);
-  else return pair_sum<OFF, N / 2>(fn) + pair_sum<OFF + N / 2, N / 2>(fn);
+  else return pair_sum<OFF, (N + 1) / 2>(fn) + pair_sum<OFF + (N + 1) / 2, N / 2>(fn);
 }
 
 // Sums of NV values per thread over each group of L consecutive threads, in
@@ -160,7 +178,7 @@ __device__ __forceinline__ void group_sum(float (&v)[NV], float *lds) {
       for (int i = 0; i < NV; ++i) lds[wave * NV + i] = v[i];
     }
     __syncthreads();
-    const float *g = lds + (wave & ~(W - 1)) * NV;
+    const float *g = lds + wave / W * W * NV;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       float t[W];
