@@ -74,14 +74,14 @@ constexpr int tpb(int L) { return L <= 128 ? 256 : L; }
 // Plain pairwise sums: with the shift and the second centring each is a sum
 // of values of the size of the spread, and 12 levels of rounding stay below
 // the result's own.
-template <class T, int L, int K, bool FULL>
+template <class T, int L, int K, int FIT>
 __global__ __launch_bounds__(tpb(L)) void k_norm_rows(
     const T *__restrict__ x, int64_t rows, int n, int64_t ldx, const void *__restrict__ w,
     const void *__restrict__ bias, int pt, double eps, T *__restrict__ y, int64_t ldy, float *__restrict__ mean,
     float *__restrict__ rstd) {
-  using Tile = svr::RowTile<T, L, K, FULL>;
+  using Tile = svr::RowTile<T, L, K, FIT>;
   constexpr int E = Tile::E, TPB = tpb(L), R = TPB / L;
-  constexpr bool HOLD = E <= 16;
+  constexpr bool HOLD = E <= 24;
   __shared__ float lds_a[TPB / 64], lds_b[2 * TPB / 64];
   const int g = threadIdx.x / L, l0 = threadIdx.x % L;
   const float inv_n = 1.0f / (float)n;
@@ -96,35 +96,36 @@ __global__ __launch_bounds__(tpb(L)) void k_norm_rows(
   }
   const int64_t step = (int64_t)gridDim.x * R;
   typename Tile::Vec raw[K];
-  T first{};
   int64_t r = (int64_t)blockIdx.x * R + g;
-  if (r < rows) {
-    Tile::load(x + r * ldx, n, Tile::avail(rows, r, ldx, n), l0, raw);
-    first = x[r * ldx];
-  }
+  int64_t rl = R == 1 || r < rows ? r : rows - 1;  // the row that is loaded
+  Tile::load(x + rl * ldx, n, Tile::avail(rows, rl, ldx, n), l0, raw);
+  T first = x[rl * ldx];
+  if constexpr (HOLD) Tile::arrived(raw, first);
   for (int64_t r0 = (int64_t)blockIdx.x * R; r0 < rows; r0 += step, r += step) {
     int l = l0;  // opaque, so that the addresses of all chunks are not kept in registers across rows
     asm volatile("" : "+v"(l));
     float f[E];
     Tile::unpack(raw, f);
-    if (r < rows) Tile::load_rest(x + r * ldx, n, Tile::avail(rows, r, ldx, n), l, f);
+    Tile::load_rest(x + rl * ldx, n, Tile::avail(rows, rl, ldx, n), l, f);
     const float x0 = svr::to_f(first);
-    if (HOLD && r + step < rows) {
-      Tile::load(x + (r + step) * ldx, n, Tile::avail(rows, r + step, ldx, n), l, raw);
-      first = x[(r + step) * ldx];
+    rl = r + step < rows ? r + step : rows - 1;
+    if constexpr (HOLD) {
+      Tile::load(x + rl * ldx, n, Tile::avail(rows, rl, ldx, n), l, raw);
+      first = x[rl * ldx];
     }
-    float a[1] = {svr::pair_sum<0, E>([&](int i) { return Tile::inside(n, l, i) ? f[i] - x0 : 0.0f; })};
+    Tile::set_rest(n, l, x0, f);
+    float a[1] = {Tile::sum(n, l, [&](int i) { return f[i] - x0; })};
     svr::group_sum<L, 1>(a, lds_a);
     const float m1 = x0 + a[0] * inv_n;
+    Tile::set_rest(n, l, m1, f);
 #pragma unroll
-    for (int i = 0; i < E; ++i) f[i] = Tile::inside(n, l, i) ? f[i] - m1 : 0.0f;
-    float s[2] = {svr::pair_sum<0, E>([&](int i) { return f[i]; }),
-                  svr::pair_sum<0, E>([&](int i) { return f[i] * f[i]; })};
+    for (int i = 0; i < E; ++i) f[i] = f[i] - m1;
+    float s[2] = {Tile::sum(n, l, [&](int i) { return f[i]; }), Tile::sum(n, l, [&](int i) { return f[i] * f[i]; })};
     svr::group_sum<L, 2>(s, lds_b);
     const float b = s[0] * inv_n;
     const float q = s[1] * inv_n - b * b;
     const float rs = rstd_of(q <= 0.0f ? 0.0f : q, eps);  // a NaN stays
-    if (r < rows) {
+    if (R == 1 || r < rows) {
       if (l == 0) {
         if (mean) mean[r] = m1 + b;
         if (rstd) rstd[r] = rs;
@@ -141,13 +142,22 @@ __global__ __launch_bounds__(tpb(L)) void k_norm_rows(
           const float ww = HOLD ? wv[HOLD ? k * VE + i : 0] : wk[i], bb = HOLD ? bv[HOLD ? k * VE + i : 0] : bk[i];
           f[k * VE + i] = ((f[k * VE + i] - b) * rs) * ww + bb;
         }
-        Tile::store_chunk(y + r * ldy, n, l, k, f);
-        if constexpr (!HOLD) __builtin_amdgcn_sched_barrier(0);
+        if constexpr (!HOLD) {
+          Tile::store_chunk(y + r * ldy, n, l, k, f);
+          __builtin_amdgcn_sched_barrier(0);
+        }
       }
     }
-    if (!HOLD && r + step < rows) {
-      Tile::load(x + (r + step) * ldx, n, Tile::avail(rows, r + step, ldx, n), l, raw);
-      first = x[(r + step) * ldx];
+    if constexpr (HOLD) {
+      Tile::arrived(raw, first);
+      if (R == 1 || r < rows) {
+#pragma unroll
+        for (int k = 0; k < K; ++k) Tile::store_chunk(y + r * ldy, n, l, k, f);
+      }
+    }
+    if constexpr (!HOLD) {
+      Tile::load(x + rl * ldx, n, Tile::avail(rows, rl, ldx, n), l, raw);
+      first = x[rl * ldx];
     }
   }
 }
@@ -162,14 +172,15 @@ bool with_tile(int64_t n, Fn &&fn) {
     fn(std::integral_constant<int, L>{}, std::integral_constant<int, K>{});        \
     return true;                                                                   \
   }
-  // up to 64 lanes with one chunk each, then whole waves with 16 values per
-  // thread, then 32 (the parameters are then read again for every row)
-  SV_TILE(1, 1) SV_TILE(2, 1) SV_TILE(4, 1) SV_TILE(8, 1) SV_TILE(16, 1) SV_TILE(32, 1) SV_TILE(64, 1)
-  if constexpr (VE == 4) { SV_TILE(64, 2) }
-  constexpr int KH = 16 / VE;
-  SV_TILE(64, KH) SV_TILE(128, KH) SV_TILE(192, KH) SV_TILE(256, KH) SV_TILE(320, KH) SV_TILE(384, KH)
-  SV_TILE(448, KH) SV_TILE(512, KH) SV_TILE(640, KH) SV_TILE(768, KH) SV_TILE(896, KH) SV_TILE(1024, KH)
-  SV_TILE(1024, 2 * KH)
+  // Up to 64 values: 8 per thread, so that a row's lanes read whole cache
+  // lines together; then 16 (half the cost per value of the cross-lane sums),
+  // or 24 where that leaves fewer threads idle; 32 for the longest rows (the
+  // parameters are then read again for every row).
+  constexpr int K8 = 8 / VE, K16 = 16 / VE, K24 = 24 / VE, K32 = 32 / VE;
+  SV_TILE(1, K8) SV_TILE(2, K8) SV_TILE(4, K8) SV_TILE(8, K8) SV_TILE(8, K16) SV_TILE(8, K24)
+  SV_TILE(16, K16) SV_TILE(16, K24) SV_TILE(32, K16) SV_TILE(32, K24) SV_TILE(64, K16) SV_TILE(64, K24)
+  SV_TILE(128, K16) SV_TILE(256, K16) SV_TILE(256, K24) SV_TILE(512, K16) SV_TILE(512, K24)
+  SV_TILE(1024, K16) SV_TILE(1024, K32)
 #undef SV_TILE
   return false;
 }
@@ -351,11 +362,14 @@ sv_status sv_layer_norm(const void *x, int dtype, int64_t rows, int64_t n, int64
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   svr::with_type(dtype, [&](auto t) {
     using T = decltype(t);
-    // an empty row has no first value to shift by (x may be NULL)
-    const bool held = n > 0 && with_tile<T>(n, [&](auto tl, auto tk) {
+    // the tiles load whole chunks of the matrix
+    const bool held = n > 0 && (rows - 1) * ldx + n >= svr::Chunk<T>::VE && with_tile<T>(n, [&](auto tl, auto tk) {
       constexpr int L = decltype(tl)::value, K = decltype(tk)::value, TPB = tpb(L), R = TPB / L;
       const int64_t blocks = (rows + R - 1) / R, most = 256 * (2048 / TPB);
-      auto *k = n == (int64_t)L * K * svr::Chunk<T>::VE ? k_norm_rows<T, L, K, true> : k_norm_rows<T, L, K, false>;
+      constexpr int VE = svr::Chunk<T>::VE;
+      auto *k = n == (int64_t)L * K * VE ? k_norm_rows<T, L, K, svr::FIT_FULL>
+                : n % VE == 0            ? k_norm_rows<T, L, K, svr::FIT_CHUNKS>
+                                         : k_norm_rows<T, L, K, svr::FIT_ANY>;
       k<<<(unsigned)(blocks < most ? blocks : most), TPB, 0, s>>>((const T *)x, rows, (int)n, ldx, weight, bias,
                                                                   param_dtype, eps, (T *)y, ldy, mean, rstd);
     });

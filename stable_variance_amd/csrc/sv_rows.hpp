@@ -53,39 +53,81 @@ struct Chunk {
   Vec v;
 };
 
+// Pairwise sum of N values fn(OFF), fn(OFF + 1), .. (adjacent pairs at each
+// level).
+template <int OFF, int N, class Fn>
+__device__ __forceinline__ float pair_sum(Fn &&fn) {
+  if constexpr (N == 1) return fn(OFF);
+  else return pair_sum<OFF, (N + 1) / 2>(fn) + pair_sum<OFF + (N + 1) / 2, N / 2>(fn);
+}
+
 // A row of n values held by L threads, K chunks each: thread l's chunk k
-// starts at value (k * L + l) * VE.  FULL: n == K * L * VE.
-template <class T, int L, int K, bool FULL>
+// starts at value (k * L + l) * VE.  FIT says what is known of n:
+//   FIT_FULL    n == K * L * VE: every chunk is whole
+//   FIT_CHUNKS  n is a multiple of VE: a chunk is whole or outside
+//   FIT_ANY     the row's last chunk may be part of one
+enum Fit { FIT_FULL = 0, FIT_CHUNKS = 1, FIT_ANY = 2 };
+
+template <class T, int L, int K, int FIT>
 struct RowTile {
   static constexpr int VE = Chunk<T>::VE, E = K * VE;
   using Vec = typename Chunk<T>::Vec;
 
-  // Values that may be read from the start of row r on (the rest of the
-  // matrix, at least n), as far as a tile needs it.
+  __device__ static __forceinline__ int first(int l, int k) { return (k * L + l) * VE; }
+  // Chunk k holds values of the row.
+  __device__ static __forceinline__ bool inside(int n, int l, int k) { return FIT == FIT_FULL || first(l, k) < n; }
+
+  // Values that may be read from the start of row r on: the rest of the
+  // matrix, at least n, cut at 2^24.
   __device__ static __forceinline__ int avail(int64_t rows, int64_t r, int64_t ld, int n) {
+    if constexpr (FIT != FIT_ANY) return n;
     const int64_t a = (rows - 1 - r) * ld + n;
     return a < (1 << 24) ? (int)a : (1 << 24);
   }
 
   // Starts the loads of the row; values past n hold anything.  The row's last
-  // chunk may reach into the next row.  Where there is none it is left out
-  // (load_rest brings it): a second way to write the same registers would
-  // make the compiler wait for the loads here.
+  // chunk may reach into the next row; where there is none, and for chunks
+  // outside the row, some other 16 bytes of the matrix are loaded (load_rest
+  // brings what is missing).  So every thread loads K chunks on every path
+  // and the compiler can leave later loads in flight when it waits for these:
+  // a load under a condition makes it wait for all.  The matrix must hold at
+  // least VE values.
   __device__ static __forceinline__ void load(const T *__restrict__ p, int n, int avail, int l, Vec (&raw)[K]) {
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      const int e = (k * L + l) * VE;
-      if (FULL || (e < n && e + VE <= avail)) __builtin_memcpy(&raw[k], p + e, 16);
+      int e = first(l, k);
+      if (FIT != FIT_FULL) {
+        const bool ok = FIT == FIT_ANY ? e < n && e + VE <= avail : e < n;
+        const int other = FIT == FIT_ANY && avail < VE ? avail - VE : 0;
+        e = ok ? e : other;
+      }
+      __builtin_memcpy(&raw[k], p + e, 16);
     }
+  }
+
+  // Waits for the loads here, so that the stores that follow are not waited
+  // for as well where the values are first used.
+  __device__ static __forceinline__ void arrived(Vec (&raw)[K], T &one) {
+    typedef unsigned U4 __attribute__((ext_vector_type(4)));
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      U4 u = __builtin_bit_cast(U4, raw[k]);
+      asm volatile("" : "+v"(u));
+      raw[k] = __builtin_bit_cast(Vec, u);
+    }
+    using Bits = std::conditional_t<sizeof(T) == 2, unsigned short, unsigned>;
+    unsigned b = __builtin_bit_cast(Bits, one);
+    asm volatile("" : "+v"(b));
+    one = __builtin_bit_cast(T, (Bits)b);
   }
 
   // The values of the last chunks that load left out.
   __device__ static __forceinline__ void load_rest(const T *__restrict__ p, int n, int avail, int l, float (&f)[E]) {
-    if constexpr (!FULL) {
+    if constexpr (FIT == FIT_ANY) {
       if (((n + VE - 1) & -VE) <= avail) return;  // the same for all lanes of a row
 #pragma unroll
       for (int k = 0; k < K; ++k) {
-        const int e = (k * L + l) * VE;
+        const int e = first(l, k);
         if (e < n && e + VE > avail) {
 #pragma unroll
           for (int i = 0; i < VE - 1; ++i)
@@ -102,23 +144,63 @@ struct RowTile {
       for (int i = 0; i < VE; ++i) f[k * VE + i] = to_f<T>(raw[k][i]);
   }
 
-  // Value i of thread l lies inside the row.
-  __device__ static __forceinline__ bool inside(int n, int l, int i) {
-    return FULL || ((i / VE) * L + l) * VE + i % VE < n;
+  // Sets what lies past n in a chunk that the row ends in.  Only the waves
+  // that hold such a chunk spend time on it.
+  __device__ static __forceinline__ void set_rest(int n, int l, float v, float (&f)[E]) {
+    if constexpr (FIT == FIT_ANY) {
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        const int left = n - first(l, k);
+        if (left > 0 && left < VE) {
+#pragma unroll
+          for (int i = 1; i < VE; ++i) f[k * VE + i] = i < left ? f[k * VE + i] : v;
+        }
+      }
+    }
+  }
+
+  // Pairwise sum of fn(value index) over the thread's values inside the row.
+  template <class Fn>
+  __device__ static __forceinline__ float sum(int n, int l, Fn &&fn) {
+    float c[K];
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      c[k] = pair_sum<0, VE>([&](int i) { return fn(k * VE + i); });
+      if (!inside(n, l, k)) c[k] = 0.0f;
+    }
+    return pair_sum<0, K>([&](int k) { return c[k]; });
   }
 
   // Chunk k of the row's values f.
   __device__ static __forceinline__ void store_chunk(T *__restrict__ p, int n, int l, int k, const float (&f)[E]) {
-    const int e = (k * L + l) * VE;
+    if (!inside(n, l, k)) return;
+    const int e = first(l, k);
     Vec v;
 #pragma unroll
     for (int i = 0; i < VE; ++i) v[i] = from_f<T>(f[k * VE + i]);
-    if (FULL || e + VE <= n) {
+    if (FIT != FIT_ANY || e + VE <= n) {
       __builtin_memcpy(p + e, &v, 16);
-    } else if (e < n) {
-#pragma unroll
-      for (int i = 0; i < VE - 1; ++i)
-        if (e + i < n) p[e + i] = v[i];
+    } else {
+      // 4, 2 and 1 of the values that are left, as their number's bits say
+      const int left = n - e;
+      typedef T V4 __attribute__((ext_vector_type(4)));
+      typedef T V2 __attribute__((ext_vector_type(2)));
+      V4 q = {v[0], v[1], v[2], v[3]};
+      T *at = p + e;
+      if constexpr (VE == 8) {
+        if (left & 4) {
+          __builtin_memcpy(at, &q, 4 * sizeof(T));
+          at += 4;
+          q = V4{v[4], v[5], v[6], v[7]};
+        }
+      }
+      V2 d = {q[0], q[1]};
+      if (left & 2) {
+        __builtin_memcpy(at, &d, 2 * sizeof(T));
+        at += 2;
+        d = V2{q[2], q[3]};
+      }
+      if (left & 1) at[0] = d[0];
     }
   }
 };
@@ -150,14 +232,6 @@ __device__ __forceinline__ void load_param(const void *__restrict__ p, int dtype
     for (int i = 0; i < VE - 1; ++i)
       if (e + i < n) out[i] = load_as(p, e + i, dtype);
   }
-}
-
-// Pairwise sum of N values fn(OFF), fn(OFF + 1), .. (adjacent pairs at each
-// level).
-template <int OFF, int N, class Fn>
-__device__ __forceinline__ float pair_sum(Fn &&fn) {
-  if constexpr (N == 1) return fn(OFF);
-  else return pair_sum<OFF, (N + 1) / 2>(fn) + pair_sum<OFF + (N + 1) / 2, N / 2>(fn);
 }
 
 // Sums of NV values per thread over each group of L consecutive threads, in
