@@ -346,5 +346,6 @@ def __getattr__(name):
     if name in ("layer_norm", "layer_norm_backward", "embedding", "embedding_backward"):
         from . import layers
 
-        return getattr(layers, name)
+        globals()[name] = fn = getattr(layers, name)
+        return fn
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

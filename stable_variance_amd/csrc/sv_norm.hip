@@ -162,25 +162,39 @@ __global__ __launch_bounds__(tpb(L)) void k_norm_rows(
   }
 }
 
-// Calls fn(L, K) (integral constants) with the smallest tile that holds n
-// values of T; false when none does.
-template <class T, class Fn>
+// Calls fn(L, K, FIT) (integral constants) with the smallest tile that holds
+// n values of T, of at most MAXL threads with MAXE values each; false
+// when none does.  The choice follows from n and the type alone.
+template <class T, int MAXL, int MAXE, class Fn>
 bool with_tile(int64_t n, Fn &&fn) {
   constexpr int VE = svr::Chunk<T>::VE;
-#define SV_TILE(L, K)                                                              \
-  if (n <= (int64_t)(L) * (K)*VE) {                                                \
-    fn(std::integral_constant<int, L>{}, std::integral_constant<int, K>{});        \
-    return true;                                                                   \
-  }
+  if (n < 1) return false;
+  const auto tile = [&](auto tl, auto tk) {
+    constexpr int L = decltype(tl)::value, K = decltype(tk)::value;
+    if constexpr (L <= MAXL && K * VE <= MAXE) {
+      if (n > (int64_t)L * K * VE) return false;
+      if constexpr (L == 1) {
+        if (n < VE) {
+          fn(tl, tk, std::integral_constant<int, svr::FIT_SMALL>{});
+          return true;
+        }
+      }
+      if (n == (int64_t)L * K * VE) fn(tl, tk, std::integral_constant<int, svr::FIT_FULL>{});
+      else if (n % VE == 0) fn(tl, tk, std::integral_constant<int, svr::FIT_CHUNKS>{});
+      else fn(tl, tk, std::integral_constant<int, svr::FIT_ANY>{});
+      return true;
+    }
+    return false;
+  };
+#define SV_TILE(L, V) \
+  if (tile(std::integral_constant<int, L>{}, std::integral_constant<int, (V) / VE>{})) return true;
   // Up to 64 values: 8 per thread, so that a row's lanes read whole cache
   // lines together; then 16 (half the cost per value of the cross-lane sums),
-  // or 24 where that leaves fewer threads idle; 32 for the longest rows (the
-  // parameters are then read again for every row).
-  constexpr int K8 = 8 / VE, K16 = 16 / VE, K24 = 24 / VE, K32 = 32 / VE;
-  SV_TILE(1, K8) SV_TILE(2, K8) SV_TILE(4, K8) SV_TILE(8, K8) SV_TILE(8, K16) SV_TILE(8, K24)
-  SV_TILE(16, K16) SV_TILE(16, K24) SV_TILE(32, K16) SV_TILE(32, K24) SV_TILE(64, K16) SV_TILE(64, K24)
-  SV_TILE(128, K16) SV_TILE(256, K16) SV_TILE(256, K24) SV_TILE(512, K16) SV_TILE(512, K24)
-  SV_TILE(1024, K16) SV_TILE(1024, K32)
+  // or 24 where that leaves fewer threads idle; 32 for the longest rows.
+  SV_TILE(1, 8) SV_TILE(2, 8) SV_TILE(4, 8) SV_TILE(8, 8) SV_TILE(8, 16) SV_TILE(8, 24)
+  SV_TILE(16, 16) SV_TILE(16, 24) SV_TILE(32, 16) SV_TILE(32, 24) SV_TILE(64, 16) SV_TILE(64, 24)
+  SV_TILE(128, 16) SV_TILE(256, 16) SV_TILE(256, 24) SV_TILE(512, 16) SV_TILE(512, 24)
+  SV_TILE(1024, 16) SV_TILE(1024, 32)
 #undef SV_TILE
   return false;
 }
@@ -220,6 +234,105 @@ __global__ __launch_bounds__(ROW_THREADS) void k_norm_any(const T *__restrict__ 
       if (w) v = v * svr::load_as(w, i, pt);
       if (bias) v = v + svr::load_as(bias, i, pt);
       yr[i] = svr::from_f<T>(v);
+    }
+  }
+}
+
+// Threads of a workgroup of the backward pass: one workgroup per CU with as
+// many waves as the registers of E values allow, since every workgroup leaves
+// one partial column sum.
+constexpr int grad_tpb(int L, int E, int VE) { return (E <= 8 ? 1024 : E <= 16 && VE == 8 && L <= 256 ? 768 : 512) / L * L; }
+constexpr int GRAD_MAXL = 512, GRAD_MAXE = 24;
+constexpr int64_t GRAD_BLOCKS = 256;  // one workgroup per CU
+// Rows that one thread adds up in plain float32 for the columns' sums; the
+// workgroup's groups and then the workgroups are joined with compensation.
+constexpr int64_t GRAD_RUN = 32;
+
+// The backward pass of rows that L threads hold (see k_norm_rows): x and dy
+// are read once.  One cross-thread sum per row gives sum(d), sum(g) and
+// sum(g d).  The column sums of the rows a group passes stay in registers;
+// at the end the workgroup's groups are added up through LDS into its row
+// of `part`, [gridDim.x][2][n] (part == nullptr: not asked for).
+template <class T, int L, int K, int FIT>
+__global__ __launch_bounds__(grad_tpb(L, K * svr::Chunk<T>::VE, svr::Chunk<T>::VE)) void k_norm_grad(
+    const T *__restrict__ dy, int64_t lddy, const T *__restrict__ x, int64_t ldx, int64_t rows, int n,
+    const void *__restrict__ w, int pt, const float *__restrict__ mean, const float *__restrict__ rstd,
+    T *__restrict__ dx, int64_t lddx, float *__restrict__ part) {
+  using Tile = svr::RowTile<T, L, K, FIT>;
+  constexpr int E = Tile::E, VE = Tile::VE, TPB = grad_tpb(L, E, VE), R = TPB / L;
+  __shared__ float lds[2][3 * TPB / 64];
+  __shared__ float cols[TPB * E];
+  const int g = threadIdx.x / L, l0 = threadIdx.x % L;
+  const float inv_n = 1.0f / (float)n;
+  float wv[E], aw[E], ab[E];
+#pragma unroll
+  for (int k = 0; k < K; ++k) svr::load_param<T, L>(w, pt, n, l0, k, 1.0f, wv + k * VE);
+#pragma unroll
+  for (int i = 0; i < E; ++i) aw[i] = ab[i] = 0.0f;
+  const int64_t step = (int64_t)gridDim.x * R;
+  typename Tile::Vec rx[K], rg[K];
+  int64_t r = (int64_t)blockIdx.x * R + g;
+  int64_t rl = R == 1 || r < rows ? r : rows - 1;  // the row that is loaded
+  Tile::load(x + rl * ldx, n, Tile::avail(rows, rl, ldx, n), l0, rx);
+  Tile::load(dy + rl * lddy, n, Tile::avail(rows, rl, lddy, n), l0, rg);
+  float m = mean[rl], rs = rstd[rl];
+  Tile::arrived(rx, m);
+  Tile::arrived(rg, rs);
+  int turn = 0;
+  for (int64_t r0 = (int64_t)blockIdx.x * R; r0 < rows; r0 += step, r += step, turn ^= 1) {
+    int l = l0;  // opaque, as in k_norm_rows
+    asm volatile("" : "+v"(l));
+    float d[E], gy[E];
+    Tile::unpack(rx, d);
+    Tile::unpack(rg, gy);
+    Tile::load_rest(x + rl * ldx, n, Tile::avail(rows, rl, ldx, n), l, d);
+    Tile::load_rest(dy + rl * lddy, n, Tile::avail(rows, rl, lddy, n), l, gy);
+    const float mu = m, rr = rs;
+    rl = r + step < rows ? r + step : rows - 1;
+    Tile::load(x + rl * ldx, n, Tile::avail(rows, rl, ldx, n), l, rx);
+    Tile::load(dy + rl * lddy, n, Tile::avail(rows, rl, lddy, n), l, rg);
+    m = mean[rl];
+    rs = rstd[rl];
+    Tile::set_rest(n, l, mu, d);
+    Tile::set_rest(n, l, 0.0f, gy);
+#pragma unroll
+    for (int i = 0; i < E; ++i) d[i] = d[i] - mu;
+    float s[3] = {Tile::sum(n, l, [&](int i) { return d[i]; }), Tile::sum(n, l, [&](int i) { return gy[i] * wv[i]; }),
+                  Tile::sum(n, l, [&](int i) { return (gy[i] * wv[i]) * d[i]; })};
+    svr::group_sum<L, 3>(s, lds[turn]);
+    const float b = s[0] * inv_n, a = s[1] * inv_n;
+    const float c = rr * ((s[2] - b * s[1]) * inv_n);
+    const bool own = R == 1 || r < rows;
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      const float xh = (d[i] - b) * rr;
+      if (own) {
+        aw[i] = aw[i] + gy[i] * xh;
+        ab[i] = ab[i] + gy[i];
+      }
+      d[i] = rr * ((gy[i] * wv[i] - a) - xh * c);
+    }
+    Tile::arrived(rx, m);
+    Tile::arrived(rg, rs);
+    if (own && dx) {
+#pragma unroll
+      for (int k = 0; k < K; ++k) Tile::store_chunk(dx + r * lddx, n, l, k, d);
+    }
+  }
+  if (!part) return;
+  for (int which = 0; which < 2; ++which) {
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+      for (int i = 0; i < VE; ++i)
+        cols[g * (L * E) + Tile::first(l0, k) + i] = which ? ab[k * VE + i] : aw[k * VE + i];
+    __syncthreads();
+    float *out = part + ((int64_t)blockIdx.x * 2 + which) * n;
+    for (int j = threadIdx.x; j < n; j += TPB) {
+      Node t = sv::zero_node();
+      for (int q = 0; q < R; ++q) svr::add_to(t, cols[q * (L * E) + j]);
+      out[j] = sv::root_value(t);
     }
   }
 }
@@ -289,24 +402,34 @@ __global__ __launch_bounds__(256) void k_norm_dw_any(const T *__restrict__ dy, i
   }
 }
 
-// Joins the groups' partial sums of 64 columns of dw (blocks [0, ctiles)) or
-// dbias (blocks [ctiles, 2 ctiles)), in group order.
-__global__ __launch_bounds__(256) void k_norm_join(const Node *__restrict__ part, int groups, int n, int ctiles,
-                                                   void *__restrict__ dw, void *__restrict__ db, int pt) {
-  __shared__ Node lds[4][64];
+__device__ __forceinline__ Node node_of(float v) { return {v, 0.0f}; }
+__device__ __forceinline__ Node node_of(Node v) { return v; }
+
+// Joins the partial sums part[groups][2][n] of 64 columns of dw (blocks [0,
+// ctiles)) or dbias (blocks [ctiles, 2 ctiles)): wave i adds up groups i,
+// i + 16, .. in order, then the waves are joined pairwise.
+constexpr int JOIN_WAVES = 16;
+template <class P>
+__global__ __launch_bounds__(64 * JOIN_WAVES) void k_norm_join(const P *__restrict__ part, int groups, int n,
+                                                               int ctiles, void *__restrict__ dw,
+                                                               void *__restrict__ db, int pt) {
+  __shared__ Node lds[JOIN_WAVES][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int which = blockIdx.x / ctiles, j = (blockIdx.x % ctiles) * 64 + lane;
+  const int which = blockIdx.x >= (unsigned)ctiles, j = ((int)blockIdx.x - which * ctiles) * 64 + lane;
+  void *out = which ? db : dw;
+  if (!out) return;
   Node s = sv::zero_node();
-  if (j < n)
-    for (int q = wave; q < groups; q += 4) s = sv::combine(s, part[((int64_t)q * 2 + which) * n + j]);
+  if (j < n) {
+#pragma unroll 8
+    for (int q = wave; q < groups; q += JOIN_WAVES) s = sv::combine(s, node_of(part[((int64_t)q * 2 + which) * n + j]));
+  }
   lds[wave][lane] = s;
   __syncthreads();
-  void *out = which ? db : dw;
-  if (wave == 0 && j < n && out) {
-    Node t[4];
+  if (wave == 0 && j < n) {
+    Node t[JOIN_WAVES];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) t[i] = lds[i][lane];
-    svr::store_as(out, j, pt, sv::root_value(sv::node_tree<0, 4, 4>(t)));
+    for (int i = 0; i < JOIN_WAVES; ++i) t[i] = lds[i][lane];
+    svr::store_as(out, j, pt, sv::root_value(sv::node_tree<0, JOIN_WAVES, JOIN_WAVES>(t)));
   }
 }
 
@@ -318,6 +441,23 @@ int64_t col_groups(int64_t rows, int64_t n) {
   if (g > COL_MAX_GROUPS) g = COL_MAX_GROUPS;
   if (g > ((int64_t)1 << 22) / ctiles) g = ((int64_t)1 << 22) / ctiles;
   return g < 1 ? 1 : g;
+}
+
+// Workgroups of k_norm_grad (0: the rows are too long for it).  Every group
+// of a workgroup passes at most GRAD_RUN rows.
+int64_t grad_blocks(int dtype, int64_t rows, int64_t n) {
+  int64_t blocks = 0;
+  svr::with_type(dtype, [&](auto t) {
+    with_tile<decltype(t), GRAD_MAXL, GRAD_MAXE>(n, [&](auto tl, auto tk, auto) {
+      constexpr int L = decltype(tl)::value, E = decltype(tk)::value * svr::Chunk<decltype(t)>::VE;
+      constexpr int64_t R = grad_tpb(L, E, svr::Chunk<decltype(t)>::VE) / L;
+      const int64_t all = (rows + R - 1) / R;
+      const int64_t rounds = (all + GRAD_RUN * GRAD_BLOCKS - 1) / (GRAD_RUN * GRAD_BLOCKS);
+      blocks = all < GRAD_BLOCKS ? all : rounds * GRAD_BLOCKS;  // whole rounds of the chip
+      if (blocks < 1) blocks = 1;
+    });
+  });
+  return blocks;
 }
 
 // Checks that the two calls share; SV_OK without touching the message.
@@ -362,16 +502,11 @@ sv_status sv_layer_norm(const void *x, int dtype, int64_t rows, int64_t n, int64
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   svr::with_type(dtype, [&](auto t) {
     using T = decltype(t);
-    // the tiles load whole chunks of the matrix
-    const bool held = n > 0 && (rows - 1) * ldx + n >= svr::Chunk<T>::VE && with_tile<T>(n, [&](auto tl, auto tk) {
+    const bool held = with_tile<T, 1024, 32>(n, [&](auto tl, auto tk, auto tf) {
       constexpr int L = decltype(tl)::value, K = decltype(tk)::value, TPB = tpb(L), R = TPB / L;
       const int64_t blocks = (rows + R - 1) / R, most = 256 * (2048 / TPB);
-      constexpr int VE = svr::Chunk<T>::VE;
-      auto *k = n == (int64_t)L * K * VE ? k_norm_rows<T, L, K, svr::FIT_FULL>
-                : n % VE == 0            ? k_norm_rows<T, L, K, svr::FIT_CHUNKS>
-                                         : k_norm_rows<T, L, K, svr::FIT_ANY>;
-      k<<<(unsigned)(blocks < most ? blocks : most), TPB, 0, s>>>((const T *)x, rows, (int)n, ldx, weight, bias,
-                                                                  param_dtype, eps, (T *)y, ldy, mean, rstd);
+      k_norm_rows<T, L, K, decltype(tf)::value><<<(unsigned)(blocks < most ? blocks : most), TPB, 0, s>>>(
+          (const T *)x, rows, (int)n, ldx, weight, bias, param_dtype, eps, (T *)y, ldy, mean, rstd);
     });
     if (held) return;
     k_norm_any<T><<<row_grid(rows), ROW_THREADS, 0, s>>>((const T *)x, rows, (int)n, ldx, weight, bias, param_dtype,
@@ -385,6 +520,8 @@ size_t sv_layer_norm_backward_workspace_size(int64_t rows, int64_t n, int dtype)
       (n > 0 && rows > svr::MAX_VALUES / n))
     return (size_t)-1;
   if (n == 0) return 0;
+  const int64_t blocks = grad_blocks(dtype, rows, n);
+  if (blocks) return svr::round256((size_t)blocks * 2 * (size_t)n * sizeof(float));
   return svr::round256((size_t)rows * 4) + (size_t)col_groups(rows, n) * 2 * (size_t)n * sizeof(Node);
 }
 
@@ -418,9 +555,27 @@ sv_status sv_layer_norm_backward(const void *dy, int64_t lddy, const void *x, in
   if ((st = check_device()) != SV_OK) return st;
   (void)hipGetLastError();
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  const int ctiles = (int)((n + 63) / 64);
+  const int64_t blocks = grad_blocks(dtype, rows, n);
+  if (blocks) {
+    float *part = cols ? reinterpret_cast<float *>(workspace) : nullptr;
+    if (rows > 0)
+      svr::with_type(dtype, [&](auto t) {
+        using T = decltype(t);
+        with_tile<T, GRAD_MAXL, GRAD_MAXE>(n, [&](auto tl, auto tk, auto tf) {
+          constexpr int L = decltype(tl)::value, K = decltype(tk)::value, TPB = grad_tpb(L, K * svr::Chunk<T>::VE, svr::Chunk<T>::VE);
+          k_norm_grad<T, L, K, decltype(tf)::value><<<(unsigned)blocks, TPB, 0, s>>>(
+              (const T *)dy, lddy, (const T *)x, ldx, rows, (int)n, weight, param_dtype, mean, rstd, (T *)dx, lddx, part);
+        });
+      });
+    if (cols)
+      k_norm_join<float><<<(unsigned)(2 * ctiles), 64 * JOIN_WAVES, 0, s>>>(part, rows > 0 ? (int)blocks : 0, (int)n,
+                                                                           ctiles, dweight, dbias, param_dtype);
+    return check_launch(who);
+  }
   float *off = cols ? reinterpret_cast<float *>(workspace) : nullptr;
   Node *part = cols ? reinterpret_cast<Node *>((char *)workspace + svr::round256((size_t)rows * 4)) : nullptr;
-  const int groups = (int)col_groups(rows, n), ctiles = (int)((n + 63) / 64);
+  const int groups = (int)col_groups(rows, n);
   svr::with_type(dtype, [&](auto t) {
     using T = decltype(t);
     const T *g = (const T *)dy, *xx = (const T *)x;
@@ -432,7 +587,8 @@ sv_status sv_layer_norm_backward(const void *dy, int64_t lddy, const void *x, in
                                                                    groups, ctiles, part);
   });
   if (cols)
-    k_norm_join<<<(unsigned)(2 * ctiles), 256, 0, s>>>(part, groups, (int)n, ctiles, dweight, dbias, param_dtype);
+    k_norm_join<Node><<<(unsigned)(2 * ctiles), 64 * JOIN_WAVES, 0, s>>>(part, groups, (int)n, ctiles, dweight,
+                                                                         dbias, param_dtype);
   return check_launch(who);
 }
 

@@ -66,7 +66,8 @@ __device__ __forceinline__ float pair_sum(Fn &&fn) {
 //   FIT_FULL    n == K * L * VE: every chunk is whole
 //   FIT_CHUNKS  n is a multiple of VE: a chunk is whole or outside
 //   FIT_ANY     the row's last chunk may be part of one
-enum Fit { FIT_FULL = 0, FIT_CHUNKS = 1, FIT_ANY = 2 };
+//   FIT_SMALL   n < VE: one thread holds the row and loads value by value
+enum Fit { FIT_FULL = 0, FIT_CHUNKS = 1, FIT_ANY = 2, FIT_SMALL = 3 };
 
 template <class T, int L, int K, int FIT>
 struct RowTile {
@@ -80,6 +81,7 @@ struct RowTile {
   // Values that may be read from the start of row r on: the rest of the
   // matrix, at least n, cut at 2^24.
   __device__ static __forceinline__ int avail(int64_t rows, int64_t r, int64_t ld, int n) {
+    if constexpr (FIT == FIT_SMALL) return 0;
     if constexpr (FIT != FIT_ANY) return n;
     const int64_t a = (rows - 1 - r) * ld + n;
     return a < (1 << 24) ? (int)a : (1 << 24);
@@ -90,9 +92,9 @@ struct RowTile {
   // outside the row, some other 16 bytes of the matrix are loaded (load_rest
   // brings what is missing).  So every thread loads K chunks on every path
   // and the compiler can leave later loads in flight when it waits for these:
-  // a load under a condition makes it wait for all.  The matrix must hold at
-  // least VE values.
+  // a load under a condition makes it wait for all.
   __device__ static __forceinline__ void load(const T *__restrict__ p, int n, int avail, int l, Vec (&raw)[K]) {
+    if constexpr (FIT == FIT_SMALL) return;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       int e = first(l, k);
@@ -107,7 +109,8 @@ struct RowTile {
 
   // Waits for the loads here, so that the stores that follow are not waited
   // for as well where the values are first used.
-  __device__ static __forceinline__ void arrived(Vec (&raw)[K], T &one) {
+  template <class S>
+  __device__ static __forceinline__ void arrived(Vec (&raw)[K], S &one) {
     typedef unsigned U4 __attribute__((ext_vector_type(4)));
 #pragma unroll
     for (int k = 0; k < K; ++k) {
@@ -115,15 +118,15 @@ struct RowTile {
       asm volatile("" : "+v"(u));
       raw[k] = __builtin_bit_cast(Vec, u);
     }
-    using Bits = std::conditional_t<sizeof(T) == 2, unsigned short, unsigned>;
+    using Bits = std::conditional_t<sizeof(S) == 2, unsigned short, unsigned>;
     unsigned b = __builtin_bit_cast(Bits, one);
     asm volatile("" : "+v"(b));
-    one = __builtin_bit_cast(T, (Bits)b);
+    one = __builtin_bit_cast(S, (Bits)b);
   }
 
   // The values of the last chunks that load left out.
   __device__ static __forceinline__ void load_rest(const T *__restrict__ p, int n, int avail, int l, float (&f)[E]) {
-    if constexpr (FIT == FIT_ANY) {
+    if constexpr (FIT == FIT_ANY || FIT == FIT_SMALL) {
       if (((n + VE - 1) & -VE) <= avail) return;  // the same for all lanes of a row
 #pragma unroll
       for (int k = 0; k < K; ++k) {
@@ -147,7 +150,7 @@ struct RowTile {
   // Sets what lies past n in a chunk that the row ends in.  Only the waves
   // that hold such a chunk spend time on it.
   __device__ static __forceinline__ void set_rest(int n, int l, float v, float (&f)[E]) {
-    if constexpr (FIT == FIT_ANY) {
+    if constexpr (FIT == FIT_ANY || FIT == FIT_SMALL) {
 #pragma unroll
       for (int k = 0; k < K; ++k) {
         const int left = n - first(l, k);
@@ -178,7 +181,7 @@ struct RowTile {
     Vec v;
 #pragma unroll
     for (int i = 0; i < VE; ++i) v[i] = from_f<T>(f[k * VE + i]);
-    if (FIT != FIT_ANY || e + VE <= n) {
+    if (FIT == FIT_FULL || FIT == FIT_CHUNKS || e + VE <= n) {
       __builtin_memcpy(p + e, &v, 16);
     } else {
       // 4, 2 and 1 of the values that are left, as their number's bits say

@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import math
 
 import torch
 
@@ -20,6 +21,10 @@ __all__ = ["layer_norm", "layer_norm_backward", "embedding", "embedding_backward
 
 _CODES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 _UNSUPPORTED = ctypes.c_size_t(-1).value
+_HERE = contextlib.nullcontext()
+# the raw stream handle without a Stream object, where torch has the call
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def _tensor(t, name, dtypes):
@@ -27,7 +32,7 @@ def _tensor(t, name, dtypes):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype not in dtypes:
         raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"{name} must be on a HIP device, got {t.device}")
 
 
@@ -38,12 +43,14 @@ def _same_device(ref, t, name):
 
 def _on(device):
     """The tensors' device, current for the launches and the allocations."""
-    return contextlib.nullcontext() if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+    return _HERE if device.index == torch.cuda.current_device() else torch.cuda.device(device)
 
 
 def _rows(t, rows, n):
     """t as [rows, n] with contiguous rows (a view where its strides allow
     one, else a copy), and its row stride."""
+    if t.is_contiguous():
+        return t, n
     t = t.detach().reshape(rows, n)
     if rows == 0 or n == 0:
         return t, n
@@ -66,10 +73,7 @@ def _shape_2d(x, name):
     if x.dim() < 1:
         raise ValueError(f"{name} needs at least one dimension")
     n = x.shape[-1]
-    rows = 1
-    for s in x.shape[:-1]:
-        rows *= s
-    return rows, n
+    return math.prod(x.shape[:-1]), n
 
 
 # ---------------------------------------------------------------- layer norm
@@ -81,7 +85,7 @@ def _param(t, name, x, n, dtype=None):
         raise ValueError(f"{name} must have shape ({n},), got {tuple(t.shape)}")
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"weight and bias must have one type, got {dtype} and {t.dtype}")
-    return t.detach().contiguous()
+    return t.contiguous()
 
 
 def _norm_forward(x, weight, bias, eps, stats):
@@ -91,14 +95,14 @@ def _norm_forward(x, weight, bias, eps, stats):
     pt = w.dtype if w is not None else b.dtype if b is not None else torch.float32
     x2, ldx = _rows(x, rows, n)
     with _on(x.device):
-        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        y = torch.empty_like(x, memory_format=torch.contiguous_format)
         mean = rstd = None
         if stats:
             mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
             rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
         _check(capi().sv_layer_norm(_ptr(x2), _CODES[x.dtype], rows, n, ldx, _ptr(w), _ptr(b), _CODES[pt], eps,
                                     _ptr(y), n, _ptr(mean), _ptr(rstd),
-                                    torch.cuda.current_stream(x.device).cuda_stream))
+                                    _raw_stream(x.device.index)))
     return y, mean, rstd
 
 
@@ -148,10 +152,10 @@ def _norm_backward(dy, x, mean, rstd, weight, need_x, need_w, need_b, param_dtyp
     w = _param(weight, "weight", x, n) if weight is not None else None
     dy2, lddy = _rows(dy, rows, n)
     x2, ldx = _rows(x, rows, n)
-    mean, rstd = mean.detach().contiguous(), rstd.detach().contiguous()
+    mean, rstd = mean.contiguous(), rstd.contiguous()
     L = capi()
     with _on(x.device):
-        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device) if need_x else None
+        dx = torch.empty_like(x, memory_format=torch.contiguous_format) if need_x else None
         dw = torch.empty(n, dtype=param_dtype, device=x.device) if need_w else None
         db = torch.empty(n, dtype=param_dtype, device=x.device) if need_b else None
         nbytes = L.sv_layer_norm_backward_workspace_size(rows, n, _CODES[x.dtype]) if need_w or need_b else 0
@@ -159,7 +163,7 @@ def _norm_backward(dy, x, mean, rstd, weight, need_x, need_w, need_b, param_dtyp
         _check(L.sv_layer_norm_backward(_ptr(dy2), lddy, _ptr(x2), ldx, _CODES[x.dtype], rows, n, _ptr(w),
                                         _CODES[param_dtype if param_dtype is not None else torch.float32], _ptr(mean),
                                         _ptr(rstd), _ptr(dx), n, _ptr(dw), _ptr(db), _ptr(ws), nbytes,
-                                        torch.cuda.current_stream(x.device).cuda_stream))
+                                        _raw_stream(x.device.index)))
     return dx, dw, db
 
 
@@ -213,7 +217,7 @@ def _lookup(ids, table, scale):
         out = torch.empty(ids.shape + (dim,), dtype=table.dtype, device=table.device)
         _check(capi().sv_embedding(_ptr(ids1), ids1.element_size(), ids1.numel(), _ptr(t2), _CODES[table.dtype], vocab,
                                    dim, ldt, scale, _ptr(out), dim,
-                                   torch.cuda.current_stream(table.device).cuda_stream))
+                                   _raw_stream(table.device.index)))
     return out
 
 
@@ -229,7 +233,7 @@ def _lookup_backward(dy, ids, vocab, scale, padding):
         ws = _scratch(nbytes, dy.device, "embedding_backward")
         _check(L.sv_embedding_backward(_ptr(dy2), lddy, _ptr(ids1), ids1.element_size(), tokens, _CODES[dy.dtype],
                                        vocab, dim, scale, padding, _ptr(grad), dim, _ptr(ws), nbytes,
-                                       torch.cuda.current_stream(dy.device).cuda_stream))
+                                       _raw_stream(dy.device.index)))
     return grad
 
 
