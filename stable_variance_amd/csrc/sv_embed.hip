@@ -29,22 +29,86 @@ constexpr int64_t MAX_VOCAB = ((int64_t)1 << 31) - 2;  // the key `vocab` fits 3
 
 // ---------------------------------------------------------------- lookup
 
-// A workgroup per token.
-template <class T>
-__global__ __launch_bounds__(256) void k_emb_lookup(const void *__restrict__ ids, int id_bytes, int64_t tokens,
-                                                    const T *__restrict__ table, int64_t vocab, int64_t dim,
-                                                    int64_t ldt, float scale, T *__restrict__ out, int64_t ldo) {
-  for (int64_t t = blockIdx.x; t < tokens; t += gridDim.x) {
-    const int64_t id = id_bytes == 8 ? reinterpret_cast<const int64_t *>(ids)[t]
-                                     : (int64_t) reinterpret_cast<const int32_t *>(ids)[t];
-    T *o = out + t * ldo;
-    if (id < 0 || id >= vocab) {
-      for (int64_t i = threadIdx.x; i < dim; i += 256) o[i] = svr::from_f<T>(__builtin_nanf(""));
-    } else {
+// A table row, an output row or a gradient row of `dim` values in chunks of
+// VE values (16 bytes; single values for dim < 16 bytes).  The last chunk is
+// moved back to end with the row: it then repeats some of the chunk before,
+// with the same bits, and no chunk needs a mask.  Chunks need the alignment
+// of T only.
+template <class T, int VE>
+struct Cols {
+  typedef T Vec __attribute__((ext_vector_type(VE)));
+
+  __device__ static __forceinline__ int64_t first(int64_t chunk, int64_t dim) {
+    const int64_t e = chunk * VE;
+    return e + VE <= dim ? e : dim - VE;
+  }
+  __device__ static __forceinline__ Vec load(const T *p) {
+    Vec v;
+    __builtin_memcpy(&v, p, sizeof(T) * VE);
+    return v;
+  }
+  __device__ static __forceinline__ void store(T *p, Vec v) { __builtin_memcpy(p, &v, sizeof(T) * VE); }
+};
+
+__device__ __forceinline__ int64_t load_id(const void *__restrict__ ids, int id_bytes, int64_t t) {
+  return id_bytes == 8 ? reinterpret_cast<const int64_t *>(ids)[t]
+                       : (int64_t) reinterpret_cast<const int32_t *>(ids)[t];
+}
+
+constexpr int THREADS = 256;
+constexpr int64_t MAX_BLOCKS = (int64_t)1 << 23;  // 2^31 work-items, within HIP's grid limit
+
+// L threads per token and tile of L * U chunks; tile u belongs to token
+// u / tiles.  All U loads are in flight together.
+template <class T, int VE, int L, int U>
+__global__ __launch_bounds__(THREADS) void k_emb_lookup(const void *__restrict__ ids, int id_bytes, int64_t units,
+                                                        int tiles, const T *__restrict__ table, int64_t vocab,
+                                                        int64_t dim, int64_t ldt, float scale, T *__restrict__ out,
+                                                        int64_t ldo) {
+  using C = Cols<T, VE>;
+  const int l = threadIdx.x % L;
+  const int64_t chunks = (dim + VE - 1) / VE;
+  for (int64_t u = (int64_t)blockIdx.x * (THREADS / L) + threadIdx.x / L; u < units;
+       u += (int64_t)gridDim.x * (THREADS / L)) {
+    const int64_t t = (unsigned)u / (unsigned)tiles, c0 = (u - t * tiles) * (L * U) + l;
+    const int64_t id = load_id(ids, id_bytes, t);
+    const bool good = id >= 0 && id < vocab;
+    typename C::Vec v[U];
+    if (good) {
       const T *r = table + id * ldt;
-      for (int64_t i = threadIdx.x; i < dim; i += 256) o[i] = svr::from_f<T>(svr::to_f(r[i]) * scale);
+#pragma unroll
+      for (int i = 0; i < U; ++i)
+        if (c0 + i * L < chunks) v[i] = C::load(r + C::first(c0 + i * L, dim));
+    }
+    T *o = out + t * ldo;
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      typename C::Vec w;
+#pragma unroll
+      for (int j = 0; j < VE; ++j)
+        w[j] = svr::from_f<T>(good ? svr::to_f<T>(v[i][j]) * scale : __builtin_nanf(""));
+      if (c0 + i * L < chunks) C::store(o + C::first(c0 + i * L, dim), w);
     }
   }
+}
+
+// Calls fn(VE, L, U) for rows of dim values: the fewest threads and chunks
+// per thread (at most 64 and MAXE values) that hold a row, else tiles of 64
+// threads with MAXE values each.
+template <class T, int MAXE, class Fn>
+void with_cols(int64_t dim, Fn &&fn) {
+  constexpr int V = 16 / (int)sizeof(T);
+  using std::integral_constant;
+  constexpr integral_constant<int, V> v{};
+  constexpr integral_constant<int, 1> one{};
+  constexpr integral_constant<int, 64> wave{};
+  if (dim < V) fn(one, integral_constant<int, 8>{}, one);
+  else if (dim <= 8 * V) fn(v, integral_constant<int, 8>{}, one);
+  else if (dim <= 16 * V) fn(v, integral_constant<int, 16>{}, one);
+  else if (dim <= 32 * V) fn(v, integral_constant<int, 32>{}, one);
+  else if (dim <= 64 * V) fn(v, wave, one);
+  else if (dim <= 128 * V || MAXE < 4 * V) fn(v, wave, integral_constant<int, 2>{});
+  else if constexpr (MAXE >= 4 * V) fn(v, wave, integral_constant<int, 4>{});
 }
 
 // ---------------------------------------------------------------- sort
@@ -78,8 +142,7 @@ SortPlan sort_plan(int64_t tokens, int64_t vocab) {
 }
 
 __device__ __forceinline__ unsigned key_of(const void *ids, int id_bytes, int64_t t, int64_t vocab, int64_t padding) {
-  const int64_t id = id_bytes == 8 ? reinterpret_cast<const int64_t *>(ids)[t]
-                                   : (int64_t) reinterpret_cast<const int32_t *>(ids)[t];
+  const int64_t id = load_id(ids, id_bytes, t);
   return id < 0 || id >= vocab || id == padding ? (unsigned)vocab : (unsigned)id;
 }
 
@@ -167,7 +230,117 @@ __global__ __launch_bounds__(SORT_THREADS) void k_sort_scatter(
   }
 }
 
+// Up to SMALL_TOKENS tokens in one workgroup and one launch: all passes in
+// LDS.  Each wave owns four runs of 64 tokens in order.
+constexpr int SMALL_RUNS = 4;
+constexpr int SMALL_TOKENS = SORT_THREADS * SMALL_RUNS;
+
+__global__ __launch_bounds__(SORT_THREADS) void k_sort_small(const void *__restrict__ ids, int id_bytes, int tokens,
+                                                             int64_t vocab, int64_t padding, int passes, int bits,
+                                                             unsigned *__restrict__ keys_out,
+                                                             int *__restrict__ tok_out) {
+  __shared__ unsigned skey[SMALL_TOKENS];
+  __shared__ unsigned short stok[SMALL_TOKENS];
+  __shared__ unsigned base[SORT_RADIX];
+  __shared__ unsigned count[SORT_WAVES][SORT_RADIX];
+  __shared__ unsigned wave_sum[SORT_WAVES];
+  const int radix = 1 << bits, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  unsigned k[SMALL_RUNS], rank[SMALL_RUNS];
+  int tok[SMALL_RUNS];
+#pragma unroll
+  for (int i = 0; i < SMALL_RUNS; ++i) {
+    const int t = wave * (64 * SMALL_RUNS) + i * 64 + lane;
+    tok[i] = t;
+    k[i] = t < tokens ? key_of(ids, id_bytes, t, vocab, padding) : 0u;
+  }
+  for (int pass = 0; pass < passes; ++pass) {
+    const int shift = pass * bits;
+    for (int i = tid; i < SORT_WAVES * radix; i += SORT_THREADS) count[i / radix][i % radix] = 0;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < SMALL_RUNS; ++i) {
+      const bool in = wave * (64 * SMALL_RUNS) + i * 64 + lane < tokens;
+      const unsigned d = (k[i] >> shift) & (radix - 1);
+      unsigned long long same = __ballot(in);
+      for (int b = 0; b < bits; ++b) {
+        const bool bit = (d >> b) & 1;
+        const unsigned long long m = __ballot(bit);
+        same &= bit ? m : ~m;
+      }
+      const unsigned r = __popcll(same & ((1ull << lane) - 1));
+      const unsigned before = count[wave][d];
+      sv::wave_lds_sync();
+      if (in && r == 0) count[wave][d] = before + __popcll(same);
+      sv::wave_lds_sync();
+      rank[i] = before + r;
+    }
+    __syncthreads();
+    // digit tid: its waves' places, then the digits' places
+    unsigned total = 0;
+    if (tid < radix) {
+#pragma unroll
+      for (int w = 0; w < SORT_WAVES; ++w) {
+        const unsigned c = count[w][tid];
+        count[w][tid] = total;
+        total += c;
+      }
+    }
+    unsigned scan = total;
+#pragma unroll
+    for (int s = 1; s < 64; s <<= 1) {
+      const unsigned v = __shfl_up(scan, s, 64);
+      if (lane >= s) scan += v;
+    }
+    if (lane == 63) wave_sum[wave] = scan;
+    __syncthreads();
+    unsigned below = 0;
+    for (int i = 0; i < wave; ++i) below += wave_sum[i];
+    if (tid < radix) base[tid] = below + scan - total;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < SMALL_RUNS; ++i) {
+      if (wave * (64 * SMALL_RUNS) + i * 64 + lane < tokens) {
+        const unsigned d = (k[i] >> shift) & (radix - 1);
+        const unsigned p = base[d] + count[wave][d] + rank[i];
+        skey[p] = k[i];
+        stok[p] = (unsigned short)tok[i];
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < SMALL_RUNS; ++i) {
+      const int t = wave * (64 * SMALL_RUNS) + i * 64 + lane;
+      if (t < tokens) {
+        k[i] = skey[t];
+        tok[i] = stok[t];
+      }
+    }
+    __syncthreads();
+  }
+#pragma unroll
+  for (int i = 0; i < SMALL_RUNS; ++i) {
+    const int t = wave * (64 * SMALL_RUNS) + i * 64 + lane;
+    if (t < tokens) {
+      keys_out[t] = k[i];
+      tok_out[t] = tok[i];
+    }
+  }
+}
+
 // ---------------------------------------------------------------- gradient
+
+// A row's tokens are the run of its key in the sorted list.  A run of up to
+// PIECE tokens is summed by one group of threads.  A longer one is cut into
+// pieces of PIECE tokens from its own start on (so the cut depends on that
+// row's tokens only); every piece leaves a node (sum and carried errors) per
+// column and a second launch joins a row's nodes in order.
+//
+// Pieces are found by block of PIECE places of the sorted list: a run longer
+// than PIECE has exactly one piece starting in every block that it crosses,
+// and a block meets at most two such runs, the one that holds its first
+// place and the one that holds its last.  Their nodes go to slots 2 b and
+// 2 b + 1 of block b.
+constexpr int PIECE = 32;
 
 // First place of the sorted keys that is not below `key`.
 __device__ __forceinline__ int lower_bound(const unsigned *__restrict__ keys, int n, unsigned key) {
@@ -180,22 +353,188 @@ __device__ __forceinline__ int lower_bound(const unsigned *__restrict__ keys, in
   return lo;
 }
 
-// A workgroup per table row.
-template <class T>
-__global__ __launch_bounds__(256) void k_emb_grad(const T *__restrict__ dy, int64_t lddy,
-                                                  const unsigned *__restrict__ keys, const int *__restrict__ tok,
-                                                  int tokens, int64_t vocab, int64_t dim, float scale,
-                                                  T *__restrict__ grad, int64_t ldg) {
-  __shared__ int ends[2];
-  for (int64_t v = blockIdx.x; v < vocab; v += gridDim.x) {
-    __syncthreads();
-    if (threadIdx.x < 2) ends[threadIdx.x] = lower_bound(keys, tokens, (unsigned)v + threadIdx.x);
-    __syncthreads();
-    const int lo = ends[0], hi = ends[1];
-    for (int64_t i = threadIdx.x; i < dim; i += 256) {
-      Node s = sv::zero_node();
-      for (int j = lo; j < hi; ++j) svr::add_to(s, svr::to_f(dy[(int64_t)tok[j] * lddy + i]));
-      grad[v * ldg + i] = svr::from_f<T>(sv::root_value(s) * scale);
+// The same node as sv::combine with a value without carry.
+__device__ __forceinline__ void add_value(Node &a, float v) {
+  const float s = a.s + v;
+  const float bv = s - a.s;
+  const float av = s - bv;
+  a.c = a.c + ((a.s - av) + (v - bv));
+  a.s = s;
+}
+
+// Adds the dy rows of the tokens at places [lo, hi) to the chunks of one
+// thread, four tokens in flight.
+template <class T, int VE, int L, int U>
+__device__ __forceinline__ void sum_run(const T *__restrict__ dy, int64_t lddy, const int *__restrict__ tok, int lo,
+                                        int hi, const int64_t (&e)[U], Node (&a)[U][VE]) {
+  using C = Cols<T, VE>;
+#pragma unroll
+  for (int i = 0; i < U; ++i)
+#pragma unroll
+    for (int j = 0; j < VE; ++j) a[i][j] = sv::zero_node();
+  for (int p = lo; p < hi; p += 4) {
+    typename C::Vec v[4][U];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int64_t t = tok[p + q < hi ? p + q : hi - 1];
+#pragma unroll
+      for (int i = 0; i < U; ++i) v[q][i] = C::load(dy + t * lddy + e[i]);
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      if (p + q < hi) {
+#pragma unroll
+        for (int i = 0; i < U; ++i)
+#pragma unroll
+          for (int j = 0; j < VE; ++j) add_value(a[i][j], svr::to_f<T>(v[q][i][j]));
+      }
+    }
+  }
+}
+
+template <class T, int VE, int L, int U>
+__device__ __forceinline__ void store_roots(T *__restrict__ row, const int64_t (&e)[U], const bool (&in)[U],
+                                            float scale, const Node (&a)[U][VE]) {
+  using C = Cols<T, VE>;
+#pragma unroll
+  for (int i = 0; i < U; ++i) {
+    typename C::Vec w;
+#pragma unroll
+    for (int j = 0; j < VE; ++j) w[j] = svr::from_f<T>(sv::root_value(a[i][j]) * scale);
+    if (in[i]) C::store(row + e[i], w);
+  }
+}
+
+// Blocks [0, pieces): a wave (or group of L threads) per block of PIECE
+// places and tile of L * U chunks.  Blocks behind: `per` consecutive
+// (row, tile) units per workgroup, rows of up to PIECE tokens.
+template <class T, int VE, int L, int U>
+__global__ __launch_bounds__(THREADS) void k_emb_grad(const T *__restrict__ dy, int64_t lddy,
+                                                      const unsigned *__restrict__ keys, const int *__restrict__ tok,
+                                                      int tokens, int64_t vocab, int64_t dim, int tiles, float scale,
+                                                      int64_t piece_blocks, int per, T *__restrict__ grad, int64_t ldg,
+                                                      Node *__restrict__ part) {
+  using C = Cols<T, VE>;
+  constexpr int G = THREADS / L;
+  __shared__ int ends[THREADS + 1];
+  const int g = threadIdx.x / L, l = threadIdx.x % L;
+  const int chunks = (int)((dim + VE - 1) / VE);
+  if (blockIdx.x < piece_blocks) {
+    const int64_t u = (int64_t)blockIdx.x * G + g;
+    const int64_t b = (unsigned)u / (unsigned)tiles;
+    const int64_t places = (tokens + PIECE - 1) / PIECE;
+    if (b >= places) return;
+    const int b0 = (int)(b * PIECE), b1 = b0 + PIECE < tokens ? b0 + PIECE : tokens;
+    int64_t e[U];
+    bool in[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int c = (int)(u - b * tiles) * (L * U) + i * L + l;
+      in[i] = c < chunks;
+      e[i] = C::first(in[i] ? c : 0, dim);
+    }
+    const unsigned kf = keys[b0], kl = keys[b1 - 1];
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+      const unsigned key = which ? kl : kf;
+      if (key >= (unsigned)vocab || (which && kl == kf)) continue;
+      // a run longer than PIECE reaches out of the block
+      const bool before = !which && b0 > 0 && keys[b0 - 1] == key;
+      const bool after = kl == key && b1 < tokens && keys[b1] == key;
+      if (!before && !after) continue;
+      const int s = lower_bound(keys, tokens, key), end = lower_bound(keys, tokens, key + 1);
+      if (end - s <= PIECE) continue;
+      const int lo = b0 <= s ? s : s + (b0 - s + PIECE - 1) / PIECE * PIECE;
+      if (lo >= end || lo >= b0 + PIECE) continue;
+      Node a[U][VE];
+      sum_run<T, VE, L, U>(dy, lddy, tok, lo, lo + PIECE < end ? lo + PIECE : end, e, a);
+      Node *o = part + (b * 2 + which) * dim;
+#pragma unroll
+      for (int i = 0; i < U; ++i)
+        if (in[i])
+#pragma unroll
+          for (int j = 0; j < VE; ++j) o[e[i] + j] = a[i][j];
+    }
+    return;
+  }
+  const int64_t units = vocab * tiles;
+  const int64_t u0 = ((int64_t)blockIdx.x - piece_blocks) * per, u1 = u0 + per < units ? u0 + per : units;
+  const int64_t v0 = (unsigned)u0 / (unsigned)tiles;
+  const int rows = (int)((unsigned)(u1 - 1) / (unsigned)tiles - v0) + 1;  // <= per
+  for (int i = threadIdx.x; i <= rows; i += THREADS) ends[i] = lower_bound(keys, tokens, (unsigned)(v0 + i));
+  __syncthreads();
+  for (int64_t u = u0 + g; u < u1; u += G) {
+    const int64_t v = (unsigned)u / (unsigned)tiles;
+    const int lo = ends[v - v0], hi = ends[v - v0 + 1];
+    if (hi - lo > PIECE) continue;
+    int64_t e[U];
+    bool in[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int c = (int)(u - v * tiles) * (L * U) + i * L + l;
+      in[i] = c < chunks;
+      e[i] = C::first(in[i] ? c : 0, dim);
+    }
+    Node a[U][VE];
+    sum_run<T, VE, L, U>(dy, lddy, tok, lo, hi, e, a);
+    store_roots<T, VE, L, U>(grad + v * ldg, e, in, scale, a);
+  }
+}
+
+// Rows of more than PIECE tokens: a workgroup per block of PIECE places and
+// tile; it works if such a run starts in its block (the run of the block's
+// last place, the only one that can).  Wave (group) i joins the i-th share
+// of the row's nodes in order, then the shares are joined pairwise.
+template <class T, int VE, int L, int U>
+__global__ __launch_bounds__(THREADS) void k_emb_join(const unsigned *__restrict__ keys, int tokens, int64_t vocab,
+                                                      int64_t dim, int tiles, unsigned blocks, float scale,
+                                                      T *__restrict__ grad, int64_t ldg,
+                                                      const Node *__restrict__ part) {
+  using C = Cols<T, VE>;
+  constexpr int G = THREADS / L;
+  __shared__ Node lds[G][L * VE];
+  const int g = threadIdx.x / L, l = threadIdx.x % L;
+  const int chunks = (int)((dim + VE - 1) / VE);
+  for (unsigned bt = blockIdx.x; bt < blocks; bt += gridDim.x) {
+    const int64_t b = bt / (unsigned)tiles;
+    const int tile = (int)(bt - b * tiles);
+    const int b0 = (int)(b * PIECE), b1 = b0 + PIECE < tokens ? b0 + PIECE : tokens;
+    const unsigned key = keys[b1 - 1];
+    if (key >= (unsigned)vocab || b1 == tokens || keys[b1] != key) continue;
+    if (b0 > 0 && keys[b0 - 1] == key) continue;
+    const int s = lower_bound(keys, tokens, key), end = lower_bound(keys, tokens, key + 1);
+    if (end - s <= PIECE) continue;
+    const int count = (end - s + PIECE - 1) / PIECE, share = (count + G - 1) / G;
+    for (int i = 0; i < U; ++i) {
+      const int c = tile * (L * U) + i * L + l;
+      const bool in = c < chunks;
+      const int64_t e = C::first(in ? c : 0, dim);
+      Node a[VE];
+  #pragma unroll
+      for (int j = 0; j < VE; ++j) a[j] = sv::zero_node();
+      const int q1 = (g + 1) * share < count ? (g + 1) * share : count;
+      for (int q = g * share; q < q1; ++q) {
+        const int at = s + q * PIECE;
+        // the run's first piece lies behind another run unless it opens its block
+        const Node *p = part + ((int64_t)(at / PIECE) * 2 + (q == 0 && s % PIECE != 0)) * dim + e;
+  #pragma unroll
+        for (int j = 0; j < VE; ++j) a[j] = sv::combine(a[j], p[j]);
+      }
+      __syncthreads();
+  #pragma unroll
+      for (int j = 0; j < VE; ++j) lds[g][l * VE + j] = a[j];
+      __syncthreads();
+      if (g == 0 && in) {
+        typename C::Vec w;
+  #pragma unroll
+        for (int j = 0; j < VE; ++j) {
+          Node t[G];
+  #pragma unroll
+          for (int q = 0; q < G; ++q) t[q] = lds[q][l * VE + j];
+          w[j] = svr::from_f<T>(sv::root_value(sv::node_tree<0, G, G>(t)) * scale);
+        }
+        C::store(grad + (int64_t)key * ldg + e, w);
+      }
     }
   }
 }
@@ -236,8 +575,13 @@ sv_status sv_embedding(const void *ids, int id_bytes, int64_t tokens, const void
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   svr::with_type(dtype, [&](auto t) {
     using T = decltype(t);
-    k_emb_lookup<T><<<(unsigned)(tokens < 65536 ? tokens : 65536), 256, 0, s>>>(
-        ids, id_bytes, tokens, (const T *)table, vocab, dim, ldt, scale, (T *)out, ldo);
+    with_cols<T, 32>(dim, [&](auto ve, auto l, auto u) {
+      constexpr int VE = decltype(ve)::value, L = decltype(l)::value, U = decltype(u)::value, G = THREADS / L;
+      const int64_t tiles = (dim + VE * L * U - 1) / (VE * L * U), units = tokens * tiles;
+      const int64_t blocks = (units + G - 1) / G;
+      k_emb_lookup<T, VE, L, U><<<(unsigned)(blocks < MAX_BLOCKS ? blocks : MAX_BLOCKS), THREADS, 0, s>>>(
+          ids, id_bytes, units, (int)tiles, (const T *)table, vocab, dim, ldt, scale, (T *)out, ldo);
+    });
   });
   return check_launch(who);
 }
@@ -247,7 +591,9 @@ size_t sv_embedding_backward_workspace_size(int64_t tokens, int64_t vocab, int64
       dim > svr::MAX_N || (dim > 0 && (tokens > svr::MAX_VALUES / dim || vocab > svr::MAX_VALUES / dim)))
     return (size_t)-1;
   if (vocab == 0 || dim == 0) return 0;
-  return 4 * svr::round256((size_t)tokens * 4) + (size_t)SORT_MAX_BLOCKS * SORT_RADIX * 4;
+  const size_t places = (size_t)(tokens + PIECE - 1) / PIECE;
+  return 4 * svr::round256((size_t)tokens * 4) + (size_t)SORT_MAX_BLOCKS * SORT_RADIX * 4 +
+         (tokens > PIECE ? places * 2 * (size_t)dim * sizeof(Node) : 0);
 }
 
 sv_status sv_embedding_backward(const void *dy, int64_t lddy, const void *ids, int id_bytes, int64_t tokens,
@@ -278,23 +624,45 @@ sv_status sv_embedding_backward(const void *dy, int64_t lddy, const void *ids, i
   unsigned *keys[2] = {(unsigned *)w, (unsigned *)(w + part)};
   int *tok[2] = {(int *)(w + 2 * part), (int *)(w + 3 * part)};
   unsigned *hist = (unsigned *)(w + 4 * part);
+  Node *nodes = (Node *)((char *)hist + (size_t)SORT_MAX_BLOCKS * SORT_RADIX * 4);
   int cur = 0;
   if (tokens > 0) {
     const SortPlan p = sort_plan(tokens, vocab);
-    for (int i = 0; i < p.passes; ++i) {
-      const unsigned *kin = i ? keys[cur] : nullptr;
-      const int *tin = i ? tok[cur] : nullptr;
-      k_sort_hist<<<p.blocks, SORT_THREADS, 0, s>>>(ids, id_bytes, kin, tokens, vocab, padding, p.span, i * p.bits,
-                                                    p.bits, hist);
-      k_sort_scatter<<<p.blocks, SORT_THREADS, 0, s>>>(ids, id_bytes, kin, tin, tokens, vocab, padding, p.span,
-                                                       i * p.bits, p.bits, hist, keys[cur ^ 1], tok[cur ^ 1]);
-      cur ^= 1;
+    if (tokens <= SMALL_TOKENS) {
+      k_sort_small<<<1, SORT_THREADS, 0, s>>>(ids, id_bytes, (int)tokens, vocab, padding, p.passes, p.bits, keys[0],
+                                              tok[0]);
+    } else {
+      for (int i = 0; i < p.passes; ++i) {
+        const unsigned *kin = i ? keys[cur] : nullptr;
+        const int *tin = i ? tok[cur] : nullptr;
+        k_sort_hist<<<p.blocks, SORT_THREADS, 0, s>>>(ids, id_bytes, kin, tokens, vocab, padding, p.span, i * p.bits,
+                                                      p.bits, hist);
+        k_sort_scatter<<<p.blocks, SORT_THREADS, 0, s>>>(ids, id_bytes, kin, tin, tokens, vocab, padding, p.span,
+                                                         i * p.bits, p.bits, hist, keys[cur ^ 1], tok[cur ^ 1]);
+        cur ^= 1;
+      }
     }
   }
   svr::with_type(dtype, [&](auto t) {
     using T = decltype(t);
-    k_emb_grad<T><<<(unsigned)(vocab < 65536 ? vocab : 65536), 256, 0, s>>>(
-        (const T *)dy, lddy, keys[cur], tok[cur], (int)tokens, vocab, dim, scale, (T *)grad, ldg);
+    with_cols<T, 16>(dim, [&](auto ve, auto l, auto u) {
+      constexpr int VE = decltype(ve)::value, L = decltype(l)::value, U = decltype(u)::value, G = THREADS / L;
+      const int64_t tiles = (dim + VE * L * U - 1) / (VE * L * U), units = vocab * tiles;
+      const int64_t places = (tokens + PIECE - 1) / PIECE;
+      const int64_t pieces = tokens > PIECE ? (places * tiles + G - 1) / G : 0;
+      // units per workgroup: about 4096 workgroups, so that the search for a
+      // row's tokens is shared by the rows of one workgroup
+      int64_t per = (units / 4096 + G - 1) / G * G;
+      per = per < G ? G : per > THREADS ? THREADS : per;
+      k_emb_grad<T, VE, L, U><<<(unsigned)(pieces + (units + per - 1) / per), THREADS, 0, s>>>(
+          (const T *)dy, lddy, keys[cur], tok[cur], (int)tokens, vocab, dim, (int)tiles, scale, pieces, (int)per,
+          (T *)grad, ldg, nodes);
+      if (pieces) {
+        const int64_t blocks = places * tiles;
+        k_emb_join<T, VE, L, U><<<(unsigned)(blocks < MAX_BLOCKS ? blocks : MAX_BLOCKS), THREADS, 0, s>>>(
+            keys[cur], (int)tokens, vocab, dim, (int)tiles, (unsigned)blocks, scale, (T *)grad, ldg, nodes);
+      }
+    });
   });
   return check_launch(who);
 }
