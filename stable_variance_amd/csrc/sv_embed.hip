@@ -175,11 +175,14 @@ __global__ __launch_bounds__(SORT_THREADS) void k_sort_scatter(
   // place of this workgroup's first token of digit tid: the digits below it
   // in all workgroups, then the same digit in the workgroups before
   unsigned total = 0, before = 0;
-  if (tid < radix)
+  if (tid < radix) {
+#pragma unroll 16
     for (int b = 0; b < (int)gridDim.x; ++b) {
-      if (b == (int)blockIdx.x) before = total;
-      total += hist[b * radix + tid];
+      const unsigned h = hist[b * radix + tid];
+      before += b < (int)blockIdx.x ? h : 0;
+      total += h;
     }
+  }
   unsigned scan = total;  // inclusive scan over the wave, then over waves
 #pragma unroll
   for (int s = 1; s < 64; s <<= 1) {
@@ -230,17 +233,17 @@ __global__ __launch_bounds__(SORT_THREADS) void k_sort_scatter(
   }
 }
 
-// Up to SMALL_TOKENS tokens in one workgroup and one launch: all passes in
-// LDS.  Each wave owns four runs of 64 tokens in order.
-constexpr int SMALL_RUNS = 4;
-constexpr int SMALL_TOKENS = SORT_THREADS * SMALL_RUNS;
+// Up to 1024 RUNS tokens in one workgroup and one launch: all passes in LDS.
+// Each wave owns RUNS runs of 64 tokens in order.
+constexpr int SMALL_TOKENS = 4 * SORT_THREADS;
 
+template <int SMALL_RUNS>
 __global__ __launch_bounds__(SORT_THREADS) void k_sort_small(const void *__restrict__ ids, int id_bytes, int tokens,
                                                              int64_t vocab, int64_t padding, int passes, int bits,
                                                              unsigned *__restrict__ keys_out,
                                                              int *__restrict__ tok_out) {
-  __shared__ unsigned skey[SMALL_TOKENS];
-  __shared__ unsigned short stok[SMALL_TOKENS];
+  __shared__ unsigned skey[SORT_THREADS * SMALL_RUNS];
+  __shared__ unsigned short stok[SORT_THREADS * SMALL_RUNS];
   __shared__ unsigned base[SORT_RADIX];
   __shared__ unsigned count[SORT_WAVES][SORT_RADIX];
   __shared__ unsigned wave_sum[SORT_WAVES];
@@ -353,6 +356,24 @@ __device__ __forceinline__ int lower_bound(const unsigned *__restrict__ keys, in
   return lo;
 }
 
+// The same, found by a group of L neighbouring threads together: each step
+// looks at L places at once.
+template <int L>
+__device__ __forceinline__ int lower_bound_group(const unsigned *__restrict__ keys, int n, unsigned key) {
+  const int l = threadIdx.x % L, shift = (threadIdx.x & 63) / L * L;
+  const unsigned long long mask = L == 64 ? ~0ull : ((1ull << (L % 64)) - 1) << shift;
+  int lo = 0, len = n;
+  while (len > 0) {
+    const int chunk = (len + L - 1) / L, first = l * chunk;  // thread l looks at the last place of its chunk
+    const int end = first + chunk < len ? first + chunk : len;
+    const int c = __popcll(__ballot(first < len && keys[first < len ? lo + end - 1 : lo] < key) & mask);
+    const int skip = c * chunk < len ? c * chunk : len;
+    lo += skip;
+    len = (chunk < len - skip ? chunk : len - skip) - 1;  // the chunk's last place is not below the key
+  }
+  return lo;
+}
+
 // The same node as sv::combine with a value without carry.
 __device__ __forceinline__ void add_value(Node &a, float v) {
   const float s = a.s + v;
@@ -406,8 +427,8 @@ __device__ __forceinline__ void store_roots(T *__restrict__ row, const int64_t (
 }
 
 // Blocks [0, pieces): a wave (or group of L threads) per block of PIECE
-// places and tile of L * U chunks.  Blocks behind: `per` consecutive
-// (row, tile) units per workgroup, rows of up to PIECE tokens.
+// places and tile of L * U chunks.  Blocks behind: `per` <= L (row, tile)
+// units per group, rows of up to PIECE tokens.
 template <class T, int VE, int L, int U>
 __global__ __launch_bounds__(THREADS) void k_emb_grad(const T *__restrict__ dy, int64_t lddy,
                                                       const unsigned *__restrict__ keys, const int *__restrict__ tok,
@@ -416,7 +437,6 @@ __global__ __launch_bounds__(THREADS) void k_emb_grad(const T *__restrict__ dy, 
                                                       Node *__restrict__ part) {
   using C = Cols<T, VE>;
   constexpr int G = THREADS / L;
-  __shared__ int ends[THREADS + 1];
   const int g = threadIdx.x / L, l = threadIdx.x % L;
   const int chunks = (int)((dim + VE - 1) / VE);
   if (blockIdx.x < piece_blocks) {
@@ -433,21 +453,23 @@ __global__ __launch_bounds__(THREADS) void k_emb_grad(const T *__restrict__ dy, 
       in[i] = c < chunks;
       e[i] = C::first(in[i] ? c : 0, dim);
     }
-    const unsigned kf = keys[b0], kl = keys[b1 - 1];
+    const unsigned kf = keys[b0], kl = keys[b1 - 1], kb = keys[b0 > 0 ? b0 - 1 : 0],
+                   ka = keys[b1 < tokens ? b1 : b1 - 1];
 #pragma unroll
     for (int which = 0; which < 2; ++which) {
       const unsigned key = which ? kl : kf;
       if (key >= (unsigned)vocab || (which && kl == kf)) continue;
       // a run longer than PIECE reaches out of the block
-      const bool before = !which && b0 > 0 && keys[b0 - 1] == key;
-      const bool after = kl == key && b1 < tokens && keys[b1] == key;
+      const bool before = !which && b0 > 0 && kb == key;
+      const bool after = kl == key && b1 < tokens && ka == key;
       if (!before && !after) continue;
-      const int s = lower_bound(keys, tokens, key), end = lower_bound(keys, tokens, key + 1);
-      if (end - s <= PIECE) continue;
+      const int s = lower_bound_group<L>(keys, tokens, key);
+      if (s + PIECE >= tokens || keys[s + PIECE] != key) continue;
       const int lo = b0 <= s ? s : s + (b0 - s + PIECE - 1) / PIECE * PIECE;
-      if (lo >= end || lo >= b0 + PIECE) continue;
+      if (lo >= b0 + PIECE || lo >= tokens || keys[lo] != key) continue;
+      const int end = lo + lower_bound(keys + lo, tokens - lo < PIECE ? tokens - lo : PIECE, key + 1);
       Node a[U][VE];
-      sum_run<T, VE, L, U>(dy, lddy, tok, lo, lo + PIECE < end ? lo + PIECE : end, e, a);
+      sum_run<T, VE, L, U>(dy, lddy, tok, lo, end, e, a);
       Node *o = part + (b * 2 + which) * dim;
 #pragma unroll
       for (int i = 0; i < U; ++i)
@@ -457,16 +479,29 @@ __global__ __launch_bounds__(THREADS) void k_emb_grad(const T *__restrict__ dy, 
     }
     return;
   }
+  // Group w of W takes units w, w + W, ..: rows that many tokens name often lie
+  // next to each other (small ids), so they go to different groups.  Thread i
+  // of the group looks up the tokens of the group's unit i.
   const int64_t units = vocab * tiles;
-  const int64_t u0 = ((int64_t)blockIdx.x - piece_blocks) * per, u1 = u0 + per < units ? u0 + per : units;
-  const int64_t v0 = (unsigned)u0 / (unsigned)tiles;
-  const int rows = (int)((unsigned)(u1 - 1) / (unsigned)tiles - v0) + 1;  // <= per
-  for (int i = threadIdx.x; i <= rows; i += THREADS) ends[i] = lower_bound(keys, tokens, (unsigned)(v0 + i));
-  __syncthreads();
-  for (int64_t u = u0 + g; u < u1; u += G) {
-    const int64_t v = (unsigned)u / (unsigned)tiles;
-    const int lo = ends[v - v0], hi = ends[v - v0 + 1];
+  const int64_t groups = ((int64_t)gridDim.x - piece_blocks) * G;
+  const int64_t w = ((int64_t)blockIdx.x - piece_blocks) * G + g;
+  int lo_of = 0, hi_of = 0;
+  if (w + l * groups < units && l < per) {
+    const unsigned v = (unsigned)(w + l * groups) / (unsigned)tiles;
+    lo_of = lower_bound(keys, tokens, v);
+    hi_of = lo_of;
+    if (lo_of < tokens && keys[lo_of] == v) {  // one past PIECE stands for any longer run
+      const int left = tokens - lo_of;
+      hi_of += lower_bound(keys + lo_of, left <= PIECE ? left : PIECE + 1, v + 1);
+    }
+  }
+  for (int k = 0; k < per; ++k) {
+    const int64_t u = w + k * groups;
+    const int lo = L == 64 ? __builtin_amdgcn_readlane(lo_of, k) : __shfl(lo_of, k, L);
+    const int hi = L == 64 ? __builtin_amdgcn_readlane(hi_of, k) : __shfl(hi_of, k, L);
+    if (u >= units) break;
     if (hi - lo > PIECE) continue;
+    const int64_t v = (unsigned)u / (unsigned)tiles;
     int64_t e[U];
     bool in[U];
 #pragma unroll
@@ -475,64 +510,90 @@ __global__ __launch_bounds__(THREADS) void k_emb_grad(const T *__restrict__ dy, 
       in[i] = c < chunks;
       e[i] = C::first(in[i] ? c : 0, dim);
     }
+    T *row = grad + v * ldg;
+    if (lo == hi) {
+      typename C::Vec zero{};
+#pragma unroll
+      for (int i = 0; i < U; ++i)
+        if (in[i]) C::store(row + e[i], zero);
+      continue;
+    }
     Node a[U][VE];
     sum_run<T, VE, L, U>(dy, lddy, tok, lo, hi, e, a);
-    store_roots<T, VE, L, U>(grad + v * ldg, e, in, scale, a);
+    store_roots<T, VE, L, U>(row, e, in, scale, a);
   }
 }
 
 // Rows of more than PIECE tokens: a workgroup per block of PIECE places and
 // tile; it works if such a run starts in its block (the run of the block's
-// last place, the only one that can).  Wave (group) i joins the i-th share
-// of the row's nodes in order, then the shares are joined pairwise.
+// last place, the only one that can).  The workgroup's groups of L threads
+// join equal shares of the row's nodes in order, then the shares are joined
+// pairwise.
+constexpr int JOIN_THREADS = 512;
 template <class T, int VE, int L, int U>
-__global__ __launch_bounds__(THREADS) void k_emb_join(const unsigned *__restrict__ keys, int tokens, int64_t vocab,
-                                                      int64_t dim, int tiles, unsigned blocks, float scale,
-                                                      T *__restrict__ grad, int64_t ldg,
-                                                      const Node *__restrict__ part) {
+__global__ __launch_bounds__(JOIN_THREADS) void k_emb_join(const unsigned *__restrict__ keys, int tokens,
+                                                           int64_t vocab, int64_t dim, int tiles, unsigned blocks,
+                                                           float scale, T *__restrict__ grad, int64_t ldg,
+                                                           const Node *__restrict__ part) {
   using C = Cols<T, VE>;
-  constexpr int G = THREADS / L;
-  __shared__ Node lds[G][L * VE];
-  const int g = threadIdx.x / L, l = threadIdx.x % L;
+  constexpr int G = JOIN_THREADS / L;
+  __shared__ Node lds[G / 2][L * VE];
+  const int g = threadIdx.x / L, l = threadIdx.x % L, lane = threadIdx.x & 63;
   const int chunks = (int)((dim + VE - 1) / VE);
   for (unsigned bt = blockIdx.x; bt < blocks; bt += gridDim.x) {
     const int64_t b = bt / (unsigned)tiles;
     const int tile = (int)(bt - b * tiles);
     const int b0 = (int)(b * PIECE), b1 = b0 + PIECE < tokens ? b0 + PIECE : tokens;
-    const unsigned key = keys[b1 - 1];
-    if (key >= (unsigned)vocab || b1 == tokens || keys[b1] != key) continue;
-    if (b0 > 0 && keys[b0 - 1] == key) continue;
-    const int s = lower_bound(keys, tokens, key), end = lower_bound(keys, tokens, key + 1);
-    if (end - s <= PIECE) continue;
-    const int count = (end - s + PIECE - 1) / PIECE, share = (count + G - 1) / G;
+    if (b1 == tokens) continue;  // no run that starts here is longer than PIECE
+    const unsigned key = keys[b1 - 1], next = keys[b1], mine = keys[b0 + lane % PIECE];
+    const unsigned last = b0 > 0 ? keys[b0 - 1] : ~key;
+    if (next != key || last == key || key >= (unsigned)vocab) continue;
+    const int s = b0 + __builtin_ctzll(__ballot(mine == key));
+    if (s + PIECE >= tokens || keys[s + PIECE] != key) continue;
+    // pieces start at s, s + PIECE, ..: those whose place still holds the key,
+    // counted by 64 and then one by one
+    int count = 1;
+    for (;;) {
+      const int64_t at = s + ((int64_t)count + 64 * lane + 63) * PIECE;
+      const unsigned long long hit = __ballot(at < tokens && keys[at < tokens ? at : 0] == key);
+      count += 64 * __popcll(hit);
+      if (~hit) break;
+    }
+    const int64_t at = s + ((int64_t)count + lane) * PIECE;
+    count += __popcll(__ballot(at < tokens && keys[at < tokens ? at : 0] == key));
+    const int share = (count + G - 1) / G;
+    const int q0 = g * share, q1 = q0 + share < count ? q0 + share : count;
     for (int i = 0; i < U; ++i) {
       const int c = tile * (L * U) + i * L + l;
       const bool in = c < chunks;
       const int64_t e = C::first(in ? c : 0, dim);
       Node a[VE];
-  #pragma unroll
+#pragma unroll
       for (int j = 0; j < VE; ++j) a[j] = sv::zero_node();
-      const int q1 = (g + 1) * share < count ? (g + 1) * share : count;
-      for (int q = g * share; q < q1; ++q) {
-        const int at = s + q * PIECE;
+#pragma unroll 2
+      for (int q = q0; q < q1; ++q) {
+        const int first = s + q * PIECE;
         // the run's first piece lies behind another run unless it opens its block
-        const Node *p = part + ((int64_t)(at / PIECE) * 2 + (q == 0 && s % PIECE != 0)) * dim + e;
-  #pragma unroll
+        const Node *p = part + ((int64_t)(first / PIECE) * 2 + (q == 0 && s != b0)) * dim + e;
+#pragma unroll
         for (int j = 0; j < VE; ++j) a[j] = sv::combine(a[j], p[j]);
       }
-      __syncthreads();
-  #pragma unroll
-      for (int j = 0; j < VE; ++j) lds[g][l * VE + j] = a[j];
-      __syncthreads();
+      for (int h = G / 2; h >= 1; h /= 2) {
+        __syncthreads();
+        if (g >= h && g < 2 * h) {
+#pragma unroll
+          for (int j = 0; j < VE; ++j) lds[g - h][l * VE + j] = a[j];
+        }
+        __syncthreads();
+        if (g < h) {
+#pragma unroll
+          for (int j = 0; j < VE; ++j) a[j] = sv::combine(a[j], lds[g][l * VE + j]);
+        }
+      }
       if (g == 0 && in) {
         typename C::Vec w;
-  #pragma unroll
-        for (int j = 0; j < VE; ++j) {
-          Node t[G];
-  #pragma unroll
-          for (int q = 0; q < G; ++q) t[q] = lds[q][l * VE + j];
-          w[j] = svr::from_f<T>(sv::root_value(sv::node_tree<0, G, G>(t)) * scale);
-        }
+#pragma unroll
+        for (int j = 0; j < VE; ++j) w[j] = svr::from_f<T>(sv::root_value(a[j]) * scale);
         C::store(grad + (int64_t)key * ldg + e, w);
       }
     }
@@ -629,8 +690,8 @@ sv_status sv_embedding_backward(const void *dy, int64_t lddy, const void *ids, i
   if (tokens > 0) {
     const SortPlan p = sort_plan(tokens, vocab);
     if (tokens <= SMALL_TOKENS) {
-      k_sort_small<<<1, SORT_THREADS, 0, s>>>(ids, id_bytes, (int)tokens, vocab, padding, p.passes, p.bits, keys[0],
-                                              tok[0]);
+      auto *k = tokens <= SORT_THREADS ? k_sort_small<1> : k_sort_small<SMALL_TOKENS / SORT_THREADS>;
+      k<<<1, SORT_THREADS, 0, s>>>(ids, id_bytes, (int)tokens, vocab, padding, p.passes, p.bits, keys[0], tok[0]);
     } else {
       for (int i = 0; i < p.passes; ++i) {
         const unsigned *kin = i ? keys[cur] : nullptr;
@@ -650,16 +711,18 @@ sv_status sv_embedding_backward(const void *dy, int64_t lddy, const void *ids, i
       const int64_t tiles = (dim + VE * L * U - 1) / (VE * L * U), units = vocab * tiles;
       const int64_t places = (tokens + PIECE - 1) / PIECE;
       const int64_t pieces = tokens > PIECE ? (places * tiles + G - 1) / G : 0;
-      // units per workgroup: about 4096 workgroups, so that the search for a
-      // row's tokens is shared by the rows of one workgroup
-      int64_t per = (units / 4096 + G - 1) / G * G;
-      per = per < G ? G : per > THREADS ? THREADS : per;
-      k_emb_grad<T, VE, L, U><<<(unsigned)(pieces + (units + per - 1) / per), THREADS, 0, s>>>(
+      // units per group: about 4096 workgroups, so that a few rows share the
+      // latency of the search for their tokens
+      constexpr int MAX_PER = L < 16 ? L : 16;
+      int64_t per = units / (4096 * G);
+      per = per < 1 ? 1 : per > MAX_PER ? MAX_PER : per;
+      const int64_t row_blocks = (units + per * G - 1) / (per * G);
+      k_emb_grad<T, VE, L, U><<<(unsigned)(pieces + row_blocks), THREADS, 0, s>>>(
           (const T *)dy, lddy, keys[cur], tok[cur], (int)tokens, vocab, dim, (int)tiles, scale, pieces, (int)per,
           (T *)grad, ldg, nodes);
       if (pieces) {
         const int64_t blocks = places * tiles;
-        k_emb_join<T, VE, L, U><<<(unsigned)(blocks < MAX_BLOCKS ? blocks : MAX_BLOCKS), THREADS, 0, s>>>(
+        k_emb_join<T, VE, L, U><<<(unsigned)(blocks < MAX_BLOCKS / 2 ? blocks : MAX_BLOCKS / 2), JOIN_THREADS, 0, s>>>(
             keys[cur], (int)tokens, vocab, dim, (int)tiles, (unsigned)blocks, scale, (T *)grad, ldg, nodes);
       }
     });
