@@ -47,7 +47,12 @@ struct Cols {
     __builtin_memcpy(&v, p, sizeof(T) * VE);
     return v;
   }
-  __device__ static __forceinline__ void store(T *p, Vec v) { __builtin_memcpy(p, &v, sizeof(T) * VE); }
+  // Non-temporal: results that nothing here reads again should not displace
+  // the rows that are read more than once.
+  __device__ static __forceinline__ void store(T *p, Vec v) {
+    typedef Vec Unaligned __attribute__((aligned(sizeof(T))));
+    __builtin_nontemporal_store(v, reinterpret_cast<Unaligned *>(p));
+  }
 };
 
 __device__ __forceinline__ int64_t load_id(const void *__restrict__ ids, int id_bytes, int64_t t) {
@@ -92,9 +97,9 @@ __global__ __launch_bounds__(THREADS) void k_emb_lookup(const void *__restrict__
   }
 }
 
-// Calls fn(VE, L, U) for rows of dim values: the fewest threads and chunks
-// per thread (at most 64 and MAXE values) that hold a row, else tiles of 64
-// threads with MAXE values each.
+// Calls fn(VE, L, U) for rows of dim values: the fewest threads that hold a
+// row with one chunk each, else tiles of 64 threads with up to MAXE values
+// each.
 template <class T, int MAXE, class Fn>
 void with_cols(int64_t dim, Fn &&fn) {
   constexpr int V = 16 / (int)sizeof(T);
@@ -102,13 +107,15 @@ void with_cols(int64_t dim, Fn &&fn) {
   constexpr integral_constant<int, V> v{};
   constexpr integral_constant<int, 1> one{};
   constexpr integral_constant<int, 64> wave{};
-  if (dim < V) fn(one, integral_constant<int, 8>{}, one);
-  else if (dim <= 8 * V) fn(v, integral_constant<int, 8>{}, one);
-  else if (dim <= 16 * V) fn(v, integral_constant<int, 16>{}, one);
-  else if (dim <= 32 * V) fn(v, integral_constant<int, 32>{}, one);
-  else if (dim <= 64 * V) fn(v, wave, one);
-  else if (dim <= 128 * V || MAXE < 4 * V) fn(v, wave, integral_constant<int, 2>{});
-  else if constexpr (MAXE >= 4 * V) fn(v, wave, integral_constant<int, 4>{});
+  if (dim < V) return fn(one, integral_constant<int, 8>{}, one);
+  if (dim <= 8 * V) return fn(v, integral_constant<int, 8>{}, one);
+  if (dim <= 16 * V) return fn(v, integral_constant<int, 16>{}, one);
+  if (dim <= 32 * V) return fn(v, integral_constant<int, 32>{}, one);
+  if constexpr (MAXE >= 4 * V)
+    if (dim > 128 * V) return fn(v, wave, integral_constant<int, 4>{});
+  if constexpr (MAXE >= 2 * V)
+    if (dim > 64 * V) return fn(v, wave, integral_constant<int, 2>{});
+  fn(v, wave, one);
 }
 
 // ---------------------------------------------------------------- sort
@@ -146,7 +153,20 @@ __device__ __forceinline__ unsigned key_of(const void *ids, int id_bytes, int64_
   return id < 0 || id >= vocab || id == padding ? (unsigned)vocab : (unsigned)id;
 }
 
+// Lanes of this wave with the same digit among those with `in` set.
+__device__ __forceinline__ unsigned long long same_digit(unsigned d, int bits, bool in) {
+  unsigned long long same = __ballot(in);
+  for (int b = 0; b < bits; ++b) {
+    const bool bit = (d >> b) & 1;
+    const unsigned long long m = __ballot(bit);
+    same &= bit ? m : ~m;
+  }
+  return same;
+}
+
 // hist[block * radix + digit].  The first pass (keys == nullptr) reads ids.
+// One lane adds for all that hold its digit: frequent tokens would otherwise
+// queue at one counter.
 __global__ __launch_bounds__(SORT_THREADS) void k_sort_hist(const void *__restrict__ ids, int id_bytes,
                                                             const unsigned *__restrict__ keys, int64_t tokens,
                                                             int64_t vocab, int64_t padding, int64_t span, int shift,
@@ -156,9 +176,13 @@ __global__ __launch_bounds__(SORT_THREADS) void k_sort_hist(const void *__restri
   if ((int)threadIdx.x < radix) h[threadIdx.x] = 0;
   __syncthreads();
   const int64_t t0 = blockIdx.x * span, t1 = t0 + span < tokens ? t0 + span : tokens;
-  for (int64_t t = t0 + threadIdx.x; t < t1; t += SORT_THREADS) {
-    const unsigned k = keys ? keys[t] : key_of(ids, id_bytes, t, vocab, padding);
-    atomicAdd(&h[(k >> shift) & (radix - 1)], 1u);
+  for (int64_t tile = t0; tile < t1; tile += SORT_THREADS) {
+    const int64_t t = tile + threadIdx.x;
+    const bool in = t < t1;
+    const unsigned k = !in ? 0u : keys ? keys[t] : key_of(ids, id_bytes, t, vocab, padding);
+    const unsigned d = (k >> shift) & (radix - 1);
+    const unsigned long long same = same_digit(d, bits, in);
+    if (in && (same & ((1ull << (threadIdx.x & 63)) - 1)) == 0) atomicAdd(&h[d], (unsigned)__popcll(same));
   }
   __syncthreads();
   if ((int)threadIdx.x < radix) hist[blockIdx.x * radix + threadIdx.x] = h[threadIdx.x];
@@ -203,13 +227,7 @@ __global__ __launch_bounds__(SORT_THREADS) void k_sort_scatter(
     const bool in = t < t1;
     const unsigned k = !in ? 0u : keys ? keys[t] : key_of(ids, id_bytes, t, vocab, padding);
     const unsigned d = (k >> shift) & (radix - 1);
-    // lanes of this wave that hold the same digit
-    unsigned long long same = __ballot(in);
-    for (int b = 0; b < bits; ++b) {
-      const bool bit = (d >> b) & 1;
-      const unsigned long long m = __ballot(bit);
-      same &= bit ? m : ~m;
-    }
+    const unsigned long long same = same_digit(d, bits, in);
     const unsigned rank = __popcll(same & ((1ull << lane) - 1));
     if (in && rank == 0) count[wave][d] = __popcll(same);
     __syncthreads();
@@ -264,12 +282,7 @@ __global__ __launch_bounds__(SORT_THREADS) void k_sort_small(const void *__restr
     for (int i = 0; i < SMALL_RUNS; ++i) {
       const bool in = wave * (64 * SMALL_RUNS) + i * 64 + lane < tokens;
       const unsigned d = (k[i] >> shift) & (radix - 1);
-      unsigned long long same = __ballot(in);
-      for (int b = 0; b < bits; ++b) {
-        const bool bit = (d >> b) & 1;
-        const unsigned long long m = __ballot(bit);
-        same &= bit ? m : ~m;
-      }
+      const unsigned long long same = same_digit(d, bits, in);
       const unsigned r = __popcll(same & ((1ull << lane) - 1));
       const unsigned before = count[wave][d];
       sv::wave_lds_sync();
@@ -344,6 +357,7 @@ __global__ __launch_bounds__(SORT_THREADS) void k_sort_small(const void *__restr
 // place and the one that holds its last.  Their nodes go to slots 2 b and
 // 2 b + 1 of block b.
 constexpr int PIECE = 32;
+constexpr int64_t WIDE_ROWS = 16384;  // rows and pieces from which tiles are wide
 
 // First place of the sorted keys that is not below `key`.
 __device__ __forceinline__ int lower_bound(const unsigned *__restrict__ keys, int n, unsigned key) {
@@ -383,8 +397,13 @@ __device__ __forceinline__ void add_value(Node &a, float v) {
   a.s = s;
 }
 
+// Lists of up to this many keys are searched in LDS: with few tokens the
+// search is most of the time.
+constexpr int LDS_KEYS = 2048;
+
 // Adds the dy rows of the tokens at places [lo, hi) to the chunks of one
-// thread, four tokens in flight.
+// thread, FLIGHT tokens' loads at a time.
+constexpr int FLIGHT = 8;
 template <class T, int VE, int L, int U>
 __device__ __forceinline__ void sum_run(const T *__restrict__ dy, int64_t lddy, const int *__restrict__ tok, int lo,
                                         int hi, const int64_t (&e)[U], Node (&a)[U][VE]) {
@@ -393,16 +412,16 @@ __device__ __forceinline__ void sum_run(const T *__restrict__ dy, int64_t lddy, 
   for (int i = 0; i < U; ++i)
 #pragma unroll
     for (int j = 0; j < VE; ++j) a[i][j] = sv::zero_node();
-  for (int p = lo; p < hi; p += 4) {
-    typename C::Vec v[4][U];
+  for (int p = lo; p < hi; p += FLIGHT) {
+    typename C::Vec v[FLIGHT][U];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
+    for (int q = 0; q < FLIGHT; ++q) {
       const int64_t t = tok[p + q < hi ? p + q : hi - 1];
 #pragma unroll
       for (int i = 0; i < U; ++i) v[q][i] = C::load(dy + t * lddy + e[i]);
     }
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
+    for (int q = 0; q < FLIGHT; ++q) {
       if (p + q < hi) {
 #pragma unroll
         for (int i = 0; i < U; ++i)
@@ -485,15 +504,24 @@ __global__ __launch_bounds__(THREADS) void k_emb_grad(const T *__restrict__ dy, 
   const int64_t units = vocab * tiles;
   const int64_t groups = ((int64_t)gridDim.x - piece_blocks) * G;
   const int64_t w = ((int64_t)blockIdx.x - piece_blocks) * G + g;
+  const bool mine = w + l * groups < units && l < per;
+  const unsigned mv = (unsigned)(mine ? w + l * groups : 0) / (unsigned)tiles;
   int lo_of = 0, hi_of = 0;
-  if (w + l * groups < units && l < per) {
-    const unsigned v = (unsigned)(w + l * groups) / (unsigned)tiles;
-    lo_of = lower_bound(keys, tokens, v);
-    hi_of = lo_of;
-    if (lo_of < tokens && keys[lo_of] == v) {  // one past PIECE stands for any longer run
+  // one past PIECE stands for any longer run
+  const auto look = [&](const unsigned *list) {
+    lo_of = hi_of = lower_bound(list, tokens, mv);
+    if (lo_of < tokens && list[lo_of] == mv) {
       const int left = tokens - lo_of;
-      hi_of += lower_bound(keys + lo_of, left <= PIECE ? left : PIECE + 1, v + 1);
+      hi_of += lower_bound(list + lo_of, left <= PIECE ? left : PIECE + 1, mv + 1);
     }
+  };
+  if (tokens <= LDS_KEYS) {
+    __shared__ unsigned list[LDS_KEYS];
+    for (int i = threadIdx.x; i < tokens; i += THREADS) list[i] = keys[i];
+    __syncthreads();
+    if (mine) look(list);
+  } else if (mine) {
+    look(keys);
   }
   for (int k = 0; k < per; ++k) {
     const int64_t u = w + k * groups;
@@ -549,18 +577,22 @@ __global__ __launch_bounds__(JOIN_THREADS) void k_emb_join(const unsigned *__res
     const unsigned last = b0 > 0 ? keys[b0 - 1] : ~key;
     if (next != key || last == key || key >= (unsigned)vocab) continue;
     const int s = b0 + __builtin_ctzll(__ballot(mine == key));
-    if (s + PIECE >= tokens || keys[s + PIECE] != key) continue;
-    // pieces start at s, s + PIECE, ..: those whose place still holds the key,
-    // counted by 64 and then one by one
-    int count = 1;
-    for (;;) {
-      const int64_t at = s + ((int64_t)count + 64 * lane + 63) * PIECE;
-      const unsigned long long hit = __ballot(at < tokens && keys[at < tokens ? at : 0] == key);
-      count += 64 * __popcll(hit);
-      if (~hit) break;
+    // pieces start at s, s + PIECE, ..: those whose place still holds the key.
+    // The first 64 at once, then by steps of 64 pieces, then the rest.
+    const auto holds = [&](int64_t piece) {
+      const int64_t at = s + piece * PIECE;
+      return __ballot(at < tokens && keys[at < tokens ? at : 0] == key);
+    };
+    int count = 1 + __popcll(holds(1 + lane));
+    if (count == 1) continue;
+    if (count == 65) {
+      unsigned long long hit;
+      do {
+        hit = holds((int64_t)count + 64 * lane + 63);
+        count += 64 * __popcll(hit);
+      } while (!~hit);
+      count += __popcll(holds((int64_t)count + lane));
     }
-    const int64_t at = s + ((int64_t)count + lane) * PIECE;
-    count += __popcll(__ballot(at < tokens && keys[at < tokens ? at : 0] == key));
     const int share = (count + G - 1) / G;
     const int q0 = g * share, q1 = q0 + share < count ? q0 + share : count;
     for (int i = 0; i < U; ++i) {
@@ -636,7 +668,7 @@ sv_status sv_embedding(const void *ids, int id_bytes, int64_t tokens, const void
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   svr::with_type(dtype, [&](auto t) {
     using T = decltype(t);
-    with_cols<T, 32>(dim, [&](auto ve, auto l, auto u) {
+    with_cols<T, 4 * (16 / (int)sizeof(T))>(dim, [&](auto ve, auto l, auto u) {
       constexpr int VE = decltype(ve)::value, L = decltype(l)::value, U = decltype(u)::value, G = THREADS / L;
       const int64_t tiles = (dim + VE * L * U - 1) / (VE * L * U), units = tokens * tiles;
       const int64_t blocks = (units + G - 1) / G;
@@ -706,7 +738,7 @@ sv_status sv_embedding_backward(const void *dy, int64_t lddy, const void *ids, i
   }
   svr::with_type(dtype, [&](auto t) {
     using T = decltype(t);
-    with_cols<T, 16>(dim, [&](auto ve, auto l, auto u) {
+    const auto go = [&](auto ve, auto l, auto u) {
       constexpr int VE = decltype(ve)::value, L = decltype(l)::value, U = decltype(u)::value, G = THREADS / L;
       const int64_t tiles = (dim + VE * L * U - 1) / (VE * L * U), units = vocab * tiles;
       const int64_t places = (tokens + PIECE - 1) / PIECE;
@@ -725,7 +757,12 @@ sv_status sv_embedding_backward(const void *dy, int64_t lddy, const void *ids, i
         k_emb_join<T, VE, L, U><<<(unsigned)(blocks < MAX_BLOCKS / 2 ? blocks : MAX_BLOCKS / 2), JOIN_THREADS, 0, s>>>(
             keys[cur], (int)tokens, vocab, dim, (int)tiles, (unsigned)blocks, scale, (T *)grad, ldg, nodes);
       }
-    });
+    };
+    // Wide tiles write longer runs of a row; narrow ones give more groups work.
+    // 64000 rows x 4096 bf16: 164 us wide, 193 narrow; 256 rows of 65536 tokens
+    // x 512 float32: 65 us wide, 58 narrow.
+    if (vocab + tokens / PIECE >= WIDE_ROWS) with_cols<T, 2 * (16 / (int)sizeof(T))>(dim, go);
+    else with_cols<T, 16 / (int)sizeof(T)>(dim, go);
   });
   return check_launch(who);
 }

@@ -31,7 +31,7 @@ using svr::Node;
 
 namespace {
 
-constexpr int ROW_THREADS = 256;
+constexpr int ROW_THREADS = 512;
 constexpr int64_t ROW_GRID = 8192;     // workgroups of a row launch, at most
 constexpr int COL_ROWS = 64;           // rows of one partial column sum
 constexpr int64_t COL_MAX_GROUPS = 512;
@@ -199,27 +199,32 @@ bool with_tile(int64_t n, Fn &&fn) {
   return false;
 }
 
-// Rows of any length: a workgroup per row, each pass reads the row again.
-// Compensated sums, as a thread adds up a long run of values one by one.
+// Rows of any length: a workgroup per row, each pass reads the row again (from
+// the cache where it fits).  Compensated sums, as a thread adds up a long run
+// of chunks one by one.
 template <class T>
 __global__ __launch_bounds__(ROW_THREADS) void k_norm_any(const T *__restrict__ x, int64_t rows, int n, int64_t ldx,
                                                           const void *__restrict__ w, const void *__restrict__ bias,
                                                           int pt, double eps, T *__restrict__ y, int64_t ldy,
                                                           float *__restrict__ mean, float *__restrict__ rstd) {
+  constexpr int VE = svr::Chunk<T>::VE;
   __shared__ Node lds[ROW_THREADS / 64];
   for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
     const T *xr = x + r * ldx;
     const float fn = (float)n;
     const float x0 = n > 0 ? svr::to_f(xr[0]) : 0.0f;
     Node a = sv::zero_node();
-    for (int i = threadIdx.x; i < n; i += ROW_THREADS) svr::add_to(a, svr::to_f(xr[i]) - x0);
+    svr::for_chunks(xr, n, threadIdx.x, ROW_THREADS, [&](int, const float *f, int count) {
+      svr::add_to(a, svr::pair_sum<0, VE>([&](int i) { return i < count ? f[i] - x0 : 0.0f; }));
+    });
     const float m1 = x0 + block_sum<ROW_THREADS / 64>(a, lds) / fn;
     Node s1 = sv::zero_node(), s2 = sv::zero_node();
-    for (int i = threadIdx.x; i < n; i += ROW_THREADS) {
-      const float d = svr::to_f(xr[i]) - m1;
-      svr::add_to(s1, d);
-      svr::add_to(s2, d * d);
-    }
+    svr::for_chunks(xr, n, threadIdx.x, ROW_THREADS, [&](int, float *f, int count) {
+#pragma unroll
+      for (int i = 0; i < VE; ++i) f[i] = i < count ? f[i] - m1 : 0.0f;
+      svr::add_to(s1, svr::pair_sum<0, VE>([&](int i) { return f[i]; }));
+      svr::add_to(s2, svr::pair_sum<0, VE>([&](int i) { return f[i] * f[i]; }));
+    });
     const float b = block_sum<ROW_THREADS / 64>(s1, lds) / fn;
     const float q = block_sum<ROW_THREADS / 64>(s2, lds) / fn - b * b;
     const float var = q <= 0.0f ? 0.0f : q;  // a NaN stays
@@ -229,12 +234,14 @@ __global__ __launch_bounds__(ROW_THREADS) void k_norm_any(const T *__restrict__ 
       if (rstd) rstd[r] = rs;
     }
     T *yr = y + r * ldy;
-    for (int i = threadIdx.x; i < n; i += ROW_THREADS) {
-      float v = ((svr::to_f(xr[i]) - m1) - b) * rs;
-      if (w) v = v * svr::load_as(w, i, pt);
-      if (bias) v = v + svr::load_as(bias, i, pt);
-      yr[i] = svr::from_f<T>(v);
-    }
+    svr::for_chunks(xr, n, threadIdx.x, ROW_THREADS, [&](int e, float *f, int count) {
+      float wv[VE], bv[VE];
+      svr::load_param<T, 1>(w, pt, n, 0, e / VE, 1.0f, wv);
+      svr::load_param<T, 1>(bias, pt, n, 0, e / VE, 0.0f, bv);
+#pragma unroll
+      for (int i = 0; i < VE; ++i) f[i] = (((f[i] - m1) - b) * rs) * wv[i] + bv[i];
+      svr::put_chunk(yr, e, count, f);
+    });
   }
 }
 
@@ -249,7 +256,9 @@ constexpr int64_t GRAD_BLOCKS = 256;  // one workgroup per CU
 constexpr int64_t GRAD_RUN = 32;
 
 // The backward pass of rows that L threads hold (see k_norm_rows): x and dy
-// are read once.  One cross-thread sum per row gives sum(d), sum(g) and
+// are read once, dx is stored non-temporal (16384 x 4096 bf16: 82 us plain, 76
+// so; the forward pass keeps plain stores, as its result is read next and
+// gains from the cache: 48 us plain, 53 non-temporal).  One cross-thread sum per row gives sum(d), sum(g) and
 // sum(g d).  The column sums of the rows a group passes stay in registers;
 // at the end the workgroup's groups are added up through LDS into its row
 // of `part`, [gridDim.x][2][n] (part == nullptr: not asked for).
@@ -316,7 +325,7 @@ __global__ __launch_bounds__(grad_tpb(L, K * svr::Chunk<T>::VE, svr::Chunk<T>::V
     Tile::arrived(rg, rs);
     if (own && dx) {
 #pragma unroll
-      for (int k = 0; k < K; ++k) Tile::store_chunk(dx + r * lddx, n, l, k, d);
+      for (int k = 0; k < K; ++k) Tile::template store_chunk<true>(dx + r * lddx, n, l, k, d);
     }
   }
   if (!part) return;
@@ -337,24 +346,39 @@ __global__ __launch_bounds__(grad_tpb(L, K * svr::Chunk<T>::VE, svr::Chunk<T>::V
   }
 }
 
-// The rows' part of the backward pass: dx and, for the column sums, b.
+// The rows' part of the backward pass for longer rows: dx and, for the column
+// sums, b.
 template <class T>
 __global__ __launch_bounds__(ROW_THREADS) void k_norm_dx_any(
     const T *__restrict__ dy, int64_t lddy, const T *__restrict__ x, int64_t ldx, int64_t rows, int n,
     const void *__restrict__ w, int pt, const float *__restrict__ mean, const float *__restrict__ rstd,
     T *__restrict__ dx, int64_t lddx, float *__restrict__ off) {
+  constexpr int VE = svr::Chunk<T>::VE;
   __shared__ Node lds[ROW_THREADS / 64];
   for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
     const T *xr = x + r * ldx, *gr = dy + r * lddy;
     const float fn = (float)n, m = mean[r], rs = rstd[r];
+    // fn(e, d, g, count) over the row's chunks
+    const auto chunks = [&](auto &&fn2) {
+      svr::for_chunks(xr, n, threadIdx.x, ROW_THREADS, [&](int e, float *d, int count) {
+        float wv[VE];
+        svr::load_param<T, 1>(w, pt, n, 0, e / VE, 1.0f, wv);
+        svr::for_chunks(gr + e, count, 0, 1, [&](int, float *g, int) {
+#pragma unroll
+          for (int i = 0; i < VE; ++i) {
+            d[i] = i < count ? d[i] - m : 0.0f;
+            g[i] = g[i] * wv[i];  // past the row 0 * 1
+          }
+          fn2(e, d, g, count);
+        });
+      });
+    };
     Node sd = sv::zero_node(), sg = sv::zero_node(), sgd = sv::zero_node();
-    for (int i = threadIdx.x; i < n; i += ROW_THREADS) {
-      const float d = svr::to_f(xr[i]) - m;
-      const float g = w ? svr::to_f(gr[i]) * svr::load_as(w, i, pt) : svr::to_f(gr[i]);
-      svr::add_to(sd, d);
-      svr::add_to(sg, g);
-      svr::add_to(sgd, g * d);
-    }
+    chunks([&](int, const float *d, const float *g, int) {
+      svr::add_to(sd, svr::pair_sum<0, VE>([&](int i) { return d[i]; }));
+      svr::add_to(sg, svr::pair_sum<0, VE>([&](int i) { return g[i]; }));
+      svr::add_to(sgd, svr::pair_sum<0, VE>([&](int i) { return g[i] * d[i]; }));
+    });
     const float b = block_sum<ROW_THREADS / 64>(sd, lds) / fn;
     const float sumg = block_sum<ROW_THREADS / 64>(sg, lds);
     const float sumgd = block_sum<ROW_THREADS / 64>(sgd, lds);
@@ -363,42 +387,64 @@ __global__ __launch_bounds__(ROW_THREADS) void k_norm_dx_any(
     if (off && threadIdx.x == 0) off[r] = b;
     if (dx) {
       T *dr = dx + r * lddx;
-      for (int i = threadIdx.x; i < n; i += ROW_THREADS) {
-        const float xh = ((svr::to_f(xr[i]) - m) - b) * rs;
-        const float g = w ? svr::to_f(gr[i]) * svr::load_as(w, i, pt) : svr::to_f(gr[i]);
-        dr[i] = svr::from_f<T>(rs * ((g - a) - xh * c));
-      }
+      chunks([&](int e, const float *d, const float *g, int count) {
+        float v[VE];
+#pragma unroll
+        for (int i = 0; i < VE; ++i) v[i] = rs * ((g[i] - a) - ((d[i] - b) * rs) * c);
+        svr::put_chunk(dr, e, count, v);
+      });
     }
   }
 }
 
-// The columns' part: group q of the rows (row r belongs to group r mod
-// groups) and 64 columns per workgroup; each wave takes every fourth row of the group.
+// The columns' part for longer rows: group q of the rows (row r belongs to
+// group r mod groups) and 64 chunks of columns per workgroup; each wave takes
+// every fourth row of the group.
+constexpr int COL_WAVES = 4;
 template <class T>
-__global__ __launch_bounds__(256) void k_norm_dw_any(const T *__restrict__ dy, int64_t lddy, const T *__restrict__ x,
-                                                     int64_t ldx, int64_t rows, int n, const float *__restrict__ mean,
-                                                     const float *__restrict__ rstd, const float *__restrict__ off,
-                                                     int groups, int ctiles, Node *__restrict__ part) {
-  __shared__ Node lds[2][4][64];
+__global__ __launch_bounds__(64 * COL_WAVES) void k_norm_dw_any(
+    const T *__restrict__ dy, int64_t lddy, const T *__restrict__ x, int64_t ldx, int64_t rows, int n,
+    const float *__restrict__ mean, const float *__restrict__ rstd, const float *__restrict__ off, int groups,
+    int ctiles, Node *__restrict__ part) {
+  constexpr int VE = svr::Chunk<T>::VE;
+  __shared__ Node lds[COL_WAVES][64][VE];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int q = blockIdx.x / ctiles, j = (blockIdx.x % ctiles) * 64 + lane;
-  Node dw = sv::zero_node(), db = sv::zero_node();
-  if (j < n) {
-    for (int64_t r = q + (int64_t)wave * groups; r < rows; r += 4 * (int64_t)groups) {
-      const float g = svr::to_f(dy[r * lddy + j]);
-      const float xh = ((svr::to_f(x[r * ldx + j]) - mean[r]) - off[r]) * rstd[r];
-      svr::add_to(dw, g * xh);
-      svr::add_to(db, g);
+  const int q = blockIdx.x / ctiles;
+  // the last chunk ends with the row and repeats some of the one before (n >= VE)
+  const int chunk = (blockIdx.x % ctiles) * 64 + lane;
+  const bool in = (int64_t)chunk * VE < n;
+  const int j = !in ? 0 : chunk * VE + VE <= n ? chunk * VE : n - VE;
+  Node dw[VE], db[VE];
+#pragma unroll
+  for (int i = 0; i < VE; ++i) dw[i] = db[i] = sv::zero_node();
+#pragma unroll 2
+  for (int64_t r = q + (int64_t)wave * groups; r < rows; r += COL_WAVES * (int64_t)groups) {
+    const float m = mean[r], b = off[r], rs = rstd[r];
+    typename svr::Chunk<T>::Vec gv, xv;
+    __builtin_memcpy(&gv, dy + r * lddy + j, 16);
+    __builtin_memcpy(&xv, x + r * ldx + j, 16);
+#pragma unroll
+    for (int i = 0; i < VE; ++i) {
+      const float g = svr::to_f<T>(gv[i]);
+      svr::add_to(dw[i], g * (((svr::to_f<T>(xv[i]) - m) - b) * rs));
+      svr::add_to(db[i], g);
     }
   }
-  lds[0][wave][lane] = dw;
-  lds[1][wave][lane] = db;
-  __syncthreads();
-  if (wave < 2 && j < n) {
-    Node t[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) t[i] = lds[wave][i][lane];
-    part[((int64_t)q * 2 + wave) * n + j] = sv::node_tree<0, 4, 4>(t);
+  for (int which = 0; which < 2; ++which) {
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < VE; ++i) lds[wave][lane][i] = which ? db[i] : dw[i];
+    __syncthreads();
+    if (wave == 0 && in) {
+#pragma unroll
+      for (int i = 0; i < VE; ++i) {
+        Node t[COL_WAVES];
+#pragma unroll
+        for (int v = 0; v < COL_WAVES; ++v) t[v] = lds[v][lane][i];
+        part[((int64_t)q * 2 + which) * n + j + i] = sv::node_tree<0, COL_WAVES, COL_WAVES>(t);
+      }
+    }
   }
 }
 
@@ -433,10 +479,16 @@ __global__ __launch_bounds__(64 * JOIN_WAVES) void k_norm_join(const P *__restri
   }
 }
 
+// Workgroups of k_norm_dw_any across a row.
+int64_t col_tiles(int dtype, int64_t n) {
+  const int64_t values = 64 * (16 / (int64_t)svr::dtype_bytes(dtype));
+  return (n + values - 1) / values;
+}
+
 // Groups of rows: 64 rows each or more, at most 512 and at most 2^22
 // workgroups in all (2^30 work-items, within HIP's grid limit).
-int64_t col_groups(int64_t rows, int64_t n) {
-  const int64_t ctiles = (n + 63) / 64;
+int64_t col_groups(int dtype, int64_t rows, int64_t n) {
+  const int64_t ctiles = col_tiles(dtype, n);
   int64_t g = (rows + COL_ROWS - 1) / COL_ROWS;
   if (g > COL_MAX_GROUPS) g = COL_MAX_GROUPS;
   if (g > ((int64_t)1 << 22) / ctiles) g = ((int64_t)1 << 22) / ctiles;
@@ -522,7 +574,7 @@ size_t sv_layer_norm_backward_workspace_size(int64_t rows, int64_t n, int dtype)
   if (n == 0) return 0;
   const int64_t blocks = grad_blocks(dtype, rows, n);
   if (blocks) return svr::round256((size_t)blocks * 2 * (size_t)n * sizeof(float));
-  return svr::round256((size_t)rows * 4) + (size_t)col_groups(rows, n) * 2 * (size_t)n * sizeof(Node);
+  return svr::round256((size_t)rows * 4) + (size_t)col_groups(dtype, rows, n) * 2 * (size_t)n * sizeof(Node);
 }
 
 sv_status sv_layer_norm_backward(const void *dy, int64_t lddy, const void *x, int64_t ldx, int dtype, int64_t rows,
@@ -575,7 +627,7 @@ sv_status sv_layer_norm_backward(const void *dy, int64_t lddy, const void *x, in
   }
   float *off = cols ? reinterpret_cast<float *>(workspace) : nullptr;
   Node *part = cols ? reinterpret_cast<Node *>((char *)workspace + svr::round256((size_t)rows * 4)) : nullptr;
-  const int groups = (int)col_groups(rows, n);
+  const int groups = (int)col_groups(dtype, rows, n), wtiles = (int)col_tiles(dtype, n);
   svr::with_type(dtype, [&](auto t) {
     using T = decltype(t);
     const T *g = (const T *)dy, *xx = (const T *)x;
@@ -583,8 +635,8 @@ sv_status sv_layer_norm_backward(const void *dy, int64_t lddy, const void *x, in
       k_norm_dx_any<T><<<row_grid(rows), ROW_THREADS, 0, s>>>(g, lddy, xx, ldx, rows, (int)n, weight, param_dtype,
                                                               mean, rstd, (T *)dx, lddx, off);
     if (cols)
-      k_norm_dw_any<T><<<(unsigned)(groups * ctiles), 256, 0, s>>>(g, lddy, xx, ldx, rows, (int)n, mean, rstd, off,
-                                                                   groups, ctiles, part);
+      k_norm_dw_any<T><<<(unsigned)(groups * wtiles), 64 * COL_WAVES, 0, s>>>(g, lddy, xx, ldx, rows, (int)n, mean,
+                                                                              rstd, off, groups, wtiles, part);
   });
   if (cols)
     k_norm_join<Node><<<(unsigned)(2 * ctiles), 64 * JOIN_WAVES, 0, s>>>(part, groups, (int)n, ctiles, dweight,

@@ -50,8 +50,55 @@ template <class T>
 struct Chunk {
   static constexpr int VE = 16 / (int)sizeof(T);
   typedef T Vec __attribute__((ext_vector_type(VE)));
-  Vec v;
 };
+
+template <bool NT, class T, class Vec>
+__device__ __forceinline__ void store16(T *p, Vec v) {
+  if constexpr (NT) {
+    typedef Vec Unaligned __attribute__((aligned(sizeof(T))));
+    __builtin_nontemporal_store(v, reinterpret_cast<Unaligned *>(p));
+  } else {
+    __builtin_memcpy(p, &v, 16);
+  }
+}
+
+// fn(e, f, count) for the chunks of a row of n values that thread `tid` of
+// `threads` passes: `count` values (VE but for the row's last chunk) from e
+// on, as float32; f may be changed and is passed on to nothing else.
+template <class T, class Fn>
+__device__ __forceinline__ void for_chunks(const T *__restrict__ p, int n, int tid, int threads, Fn &&fn) {
+  constexpr int VE = Chunk<T>::VE;
+  for (int e = tid * VE; e < n; e += threads * VE) {
+    float f[VE];
+    const int count = n - e < VE ? n - e : VE;
+    if (count == VE) {
+      typename Chunk<T>::Vec v;
+      __builtin_memcpy(&v, p + e, 16);
+#pragma unroll
+      for (int i = 0; i < VE; ++i) f[i] = to_f<T>(v[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < VE; ++i) f[i] = i < count ? to_f<T>(p[e + i]) : 0.0f;
+    }
+    fn(e, f, count);
+  }
+}
+
+// The chunk back: `count` values of f at p + e.
+template <class T>
+__device__ __forceinline__ void put_chunk(T *__restrict__ p, int e, int count, const float *f) {
+  constexpr int VE = Chunk<T>::VE;
+  typename Chunk<T>::Vec v;
+#pragma unroll
+  for (int i = 0; i < VE; ++i) v[i] = from_f<T>(f[i]);
+  if (count == VE) {
+    __builtin_memcpy(p + e, &v, 16);
+  } else {
+#pragma unroll
+    for (int i = 0; i < VE - 1; ++i)
+      if (i < count) p[e + i] = v[i];
+  }
+}
 
 // Pairwise sum of N values fn(OFF), fn(OFF + 1), .. (adjacent pairs at each
 // level).
@@ -174,7 +221,8 @@ struct RowTile {
     return pair_sum<0, K>([&](int k) { return c[k]; });
   }
 
-  // Chunk k of the row's values f.
+  // Chunk k of the row's values f.  NT: non-temporal.
+  template <bool NT = false>
   __device__ static __forceinline__ void store_chunk(T *__restrict__ p, int n, int l, int k, const float (&f)[E]) {
     if (!inside(n, l, k)) return;
     const int e = first(l, k);
@@ -182,7 +230,7 @@ struct RowTile {
 #pragma unroll
     for (int i = 0; i < VE; ++i) v[i] = from_f<T>(f[k * VE + i]);
     if (FIT == FIT_FULL || FIT == FIT_CHUNKS || e + VE <= n) {
-      __builtin_memcpy(p + e, &v, 16);
+      store16<NT>(p + e, v);
     } else {
       // 4, 2 and 1 of the values that are left, as their number's bits say
       const int left = n - e;
