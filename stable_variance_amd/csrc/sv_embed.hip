@@ -121,13 +121,13 @@ void with_cols(int64_t dim, Fn &&fn) {
 // ---------------------------------------------------------------- sort
 
 // Up to 64 workgroups of 1024 threads, each owning one run of `span` tokens
-// (a multiple of 1024).  A digit of `bits` <= 9 bits takes two launches: the
+// (a multiple of 1024).  A digit of `bits` <= 10 bits takes two launches: the
 // workgroups' histograms, then the scatter, where each workgroup finds its
 // digits' places from all histograms.
 constexpr int SORT_THREADS = 1024;
 constexpr int SORT_WAVES = SORT_THREADS / 64;
 constexpr int SORT_MAX_BLOCKS = 64;
-constexpr int SORT_MAX_BITS = 9;
+constexpr int SORT_MAX_BITS = 10;
 constexpr int SORT_RADIX = 1 << SORT_MAX_BITS;
 
 struct SortPlan {
@@ -191,11 +191,22 @@ __global__ __launch_bounds__(SORT_THREADS) void k_sort_hist(const void *__restri
 __global__ __launch_bounds__(SORT_THREADS) void k_sort_scatter(
     const void *__restrict__ ids, int id_bytes, const unsigned *__restrict__ keys, const int *__restrict__ tok,
     int64_t tokens, int64_t vocab, int64_t padding, int64_t span, int shift, int bits,
-    const unsigned *__restrict__ hist, unsigned *__restrict__ keys_out, int *__restrict__ tok_out) {
+    const unsigned *__restrict__ hist, unsigned *__restrict__ keys_out, int *__restrict__ tok_out,
+    unsigned *__restrict__ sample, int sample_shift) {
   __shared__ unsigned base[SORT_RADIX];
   __shared__ unsigned count[SORT_WAVES][SORT_RADIX];
   __shared__ unsigned wave_sum[SORT_WAVES];
   const int radix = 1 << bits, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int64_t t0 = blockIdx.x * span, t1 = t0 + span < tokens ? t0 + span : tokens;
+  unsigned k_next = 0;
+  int tok_next = 0;
+  const auto load = [&](int64_t t) {
+    if (t < t1) {
+      k_next = keys ? keys[t] : key_of(ids, id_bytes, t, vocab, padding);
+      tok_next = tok ? tok[t] : (int)t;
+    }
+  };
+  load(t0 + tid);  // in flight while the places are added up
   // place of this workgroup's first token of digit tid: the digits below it
   // in all workgroups, then the same digit in the workgroups before
   unsigned total = 0, before = 0;
@@ -219,13 +230,13 @@ __global__ __launch_bounds__(SORT_THREADS) void k_sort_scatter(
   for (int i = 0; i < wave; ++i) below += wave_sum[i];
   if (tid < radix) base[tid] = below + scan - total + before;
 
-  const int64_t t0 = blockIdx.x * span, t1 = t0 + span < tokens ? t0 + span : tokens;
   for (int64_t tile = t0; tile < t1; tile += SORT_THREADS) {
     for (int i = tid; i < SORT_WAVES * radix; i += SORT_THREADS) count[i / radix][i % radix] = 0;
     __syncthreads();
-    const int64_t t = tile + tid;
-    const bool in = t < t1;
-    const unsigned k = !in ? 0u : keys ? keys[t] : key_of(ids, id_bytes, t, vocab, padding);
+    const bool in = tile + tid < t1;
+    const unsigned k = in ? k_next : 0u;
+    const int this_tok = tok_next;
+    load(tile + SORT_THREADS + tid);
     const unsigned d = (k >> shift) & (radix - 1);
     const unsigned long long same = same_digit(d, bits, in);
     const unsigned rank = __popcll(same & ((1ull << lane) - 1));
@@ -245,7 +256,8 @@ __global__ __launch_bounds__(SORT_THREADS) void k_sort_scatter(
     if (in) {
       const unsigned p = count[wave][d] + rank;
       keys_out[p] = k;
-      tok_out[p] = tok ? tok[t] : (int)t;
+      tok_out[p] = this_tok;
+      if (sample && (p & ((1u << sample_shift) - 1)) == 0) sample[p >> sample_shift] = k;
     }
     __syncthreads();
   }
@@ -370,22 +382,47 @@ __device__ __forceinline__ int lower_bound(const unsigned *__restrict__ keys, in
   return lo;
 }
 
-// The same, found by a group of L neighbouring threads together: each step
-// looks at L places at once.
+// Lanes of a wave that belong to this thread's group of L.
+template <int L>
+__device__ __forceinline__ unsigned long long group_lanes() {
+  return L == 64 ? ~0ull : ((1ull << (L % 64)) - 1) << ((threadIdx.x & 63) / L * L);
+}
+
+// lower_bound by a group of L neighbouring threads together: each step looks
+// at L places at once.
 template <int L>
 __device__ __forceinline__ int lower_bound_group(const unsigned *__restrict__ keys, int n, unsigned key) {
-  const int l = threadIdx.x % L, shift = (threadIdx.x & 63) / L * L;
-  const unsigned long long mask = L == 64 ? ~0ull : ((1ull << (L % 64)) - 1) << shift;
+  const int l = threadIdx.x % L;
   int lo = 0, len = n;
   while (len > 0) {
     const int chunk = (len + L - 1) / L, first = l * chunk;  // thread l looks at the last place of its chunk
     const int end = first + chunk < len ? first + chunk : len;
-    const int c = __popcll(__ballot(first < len && keys[first < len ? lo + end - 1 : lo] < key) & mask);
+    const int c = __popcll(__ballot(first < len && keys[first < len ? lo + end - 1 : lo] < key) & group_lanes<L>());
     const int skip = c * chunk < len ? c * chunk : len;
     lo += skip;
     len = (chunk < len - skip ? chunk : len - skip) - 1;  // the chunk's last place is not below the key
   }
   return lo;
+}
+
+// The piece of `key`'s run that starts in the block of places [b0, b0 +
+// PIECE), [lo, end), found by a group; end == lo if there is none (no run of
+// more than PIECE, or none of its pieces starts here).
+template <int L>
+__device__ __forceinline__ void find_piece(const unsigned *__restrict__ keys, int tokens, unsigned key, int b0,
+                                           int &lo, int &end) {
+  const int l = threadIdx.x % L;
+  const int s = lower_bound_group<L>(keys, tokens, key);
+  lo = b0 <= s ? s : s + (b0 - s + PIECE - 1) / PIECE * PIECE;
+  const unsigned beyond = keys[s + PIECE < tokens ? s + PIECE : 0];
+  int held = 0;
+#pragma unroll
+  for (int i = 0; i < PIECE; i += L) {
+    const int at = lo + i + l;
+    const unsigned k = keys[at < tokens ? at : 0];
+    held += __popcll(__ballot(i + l < PIECE && at < tokens && k == key) & group_lanes<L>());
+  }
+  end = s + PIECE < tokens && beyond == key && lo < b0 + PIECE ? lo + held : lo;
 }
 
 // The same node as sv::combine with a value without carry.
@@ -397,9 +434,9 @@ __device__ __forceinline__ void add_value(Node &a, float v) {
   a.s = s;
 }
 
-// Lists of up to this many keys are searched in LDS: with few tokens the
-// search is most of the time.
-constexpr int LDS_KEYS = 2048;
+// Keys that the search for a row's tokens finds in LDS: the whole list, or
+// every 2^sample_shift-th key, which leaves a few steps in memory.
+constexpr int LDS_KEYS = 4096;
 
 // Adds the dy rows of the tokens at places [lo, hi) to the chunks of one
 // thread, FLIGHT tokens' loads at a time.
@@ -451,13 +488,19 @@ __device__ __forceinline__ void store_roots(T *__restrict__ row, const int64_t (
 template <class T, int VE, int L, int U>
 __global__ __launch_bounds__(THREADS) void k_emb_grad(const T *__restrict__ dy, int64_t lddy,
                                                       const unsigned *__restrict__ keys, const int *__restrict__ tok,
+                                                      const unsigned *__restrict__ sample, int sample_shift,
                                                       int tokens, int64_t vocab, int64_t dim, int tiles, float scale,
                                                       int64_t piece_blocks, int per, T *__restrict__ grad, int64_t ldg,
                                                       Node *__restrict__ part) {
   using C = Cols<T, VE>;
   constexpr int G = THREADS / L;
+  __shared__ unsigned list[LDS_KEYS];
   const int g = threadIdx.x / L, l = threadIdx.x % L;
   const int chunks = (int)((dim + VE - 1) / VE);
+  const int samples = (tokens + (1 << sample_shift) - 1) >> sample_shift;  // <= LDS_KEYS
+#pragma unroll 4
+  for (int i = threadIdx.x; i < samples; i += THREADS) list[i] = sample[i];
+  __syncthreads();
   if (blockIdx.x < piece_blocks) {
     const int64_t u = (int64_t)blockIdx.x * G + g;
     const int64_t b = (unsigned)u / (unsigned)tiles;
@@ -472,21 +515,26 @@ __global__ __launch_bounds__(THREADS) void k_emb_grad(const T *__restrict__ dy, 
       in[i] = c < chunks;
       e[i] = C::first(in[i] ? c : 0, dim);
     }
-    const unsigned kf = keys[b0], kl = keys[b1 - 1], kb = keys[b0 > 0 ? b0 - 1 : 0],
-                   ka = keys[b1 < tokens ? b1 : b1 - 1];
+    int plo[2] = {0, 0}, pend[2] = {0, 0};
+    const auto plan = [&](const unsigned *list) {
+      const unsigned kf = list[b0], kl = list[b1 - 1], kb = list[b0 > 0 ? b0 - 1 : 0],
+                     ka = list[b1 < tokens ? b1 : b1 - 1];
+#pragma unroll
+      for (int which = 0; which < 2; ++which) {
+        const unsigned key = which ? kl : kf;
+        // a run longer than PIECE reaches out of the block
+        const bool before = !which && b0 > 0 && kb == key;
+        const bool after = kl == key && b1 < tokens && ka == key;
+        if (key < (unsigned)vocab && (before || after) && !(which && kl == kf))
+          find_piece<L>(list, tokens, key, b0, plo[which], pend[which]);
+      }
+    };
+    if (sample_shift == 0) plan(list);
+    else plan(keys);
 #pragma unroll
     for (int which = 0; which < 2; ++which) {
-      const unsigned key = which ? kl : kf;
-      if (key >= (unsigned)vocab || (which && kl == kf)) continue;
-      // a run longer than PIECE reaches out of the block
-      const bool before = !which && b0 > 0 && kb == key;
-      const bool after = kl == key && b1 < tokens && ka == key;
-      if (!before && !after) continue;
-      const int s = lower_bound_group<L>(keys, tokens, key);
-      if (s + PIECE >= tokens || keys[s + PIECE] != key) continue;
-      const int lo = b0 <= s ? s : s + (b0 - s + PIECE - 1) / PIECE * PIECE;
-      if (lo >= b0 + PIECE || lo >= tokens || keys[lo] != key) continue;
-      const int end = lo + lower_bound(keys + lo, tokens - lo < PIECE ? tokens - lo : PIECE, key + 1);
+      const int lo = plo[which], end = pend[which];
+      if (lo == end) continue;
       Node a[U][VE];
       sum_run<T, VE, L, U>(dy, lddy, tok, lo, end, e, a);
       Node *o = part + (b * 2 + which) * dim;
@@ -508,20 +556,22 @@ __global__ __launch_bounds__(THREADS) void k_emb_grad(const T *__restrict__ dy, 
   const unsigned mv = (unsigned)(mine ? w + l * groups : 0) / (unsigned)tiles;
   int lo_of = 0, hi_of = 0;
   // one past PIECE stands for any longer run
-  const auto look = [&](const unsigned *list) {
-    lo_of = hi_of = lower_bound(list, tokens, mv);
-    if (lo_of < tokens && list[lo_of] == mv) {
+  const auto look = [&](const unsigned *keys, int from, int n) {
+    lo_of = hi_of = from + lower_bound(keys + from, n, mv);
+    if (lo_of < tokens && keys[lo_of] == mv) {
       const int left = tokens - lo_of;
-      hi_of += lower_bound(list + lo_of, left <= PIECE ? left : PIECE + 1, mv + 1);
+      hi_of += lower_bound(keys + lo_of, left <= PIECE ? left : PIECE + 1, mv + 1);
     }
   };
-  if (tokens <= LDS_KEYS) {
-    __shared__ unsigned list[LDS_KEYS];
-    for (int i = threadIdx.x; i < tokens; i += THREADS) list[i] = keys[i];
-    __syncthreads();
-    if (mine) look(list);
-  } else if (mine) {
-    look(keys);
+  if (mine) {
+    if (sample_shift == 0) {
+      look(list, 0, tokens);
+    } else {  // behind the last sample below the row's key, up to the next sample
+      const int i = lower_bound(list, samples, mv);
+      const int from = i > 0 ? ((i - 1) << sample_shift) + 1 : 0;
+      const int to = (i << sample_shift) < tokens ? i << sample_shift : tokens;
+      look(keys, from, to - from);
+    }
   }
   for (int k = 0; k < per; ++k) {
     const int64_t u = w + k * groups;
@@ -685,7 +735,7 @@ size_t sv_embedding_backward_workspace_size(int64_t tokens, int64_t vocab, int64
     return (size_t)-1;
   if (vocab == 0 || dim == 0) return 0;
   const size_t places = (size_t)(tokens + PIECE - 1) / PIECE;
-  return 4 * svr::round256((size_t)tokens * 4) + (size_t)SORT_MAX_BLOCKS * SORT_RADIX * 4 +
+  return 4 * svr::round256((size_t)tokens * 4) + (size_t)(SORT_MAX_BLOCKS * SORT_RADIX + LDS_KEYS) * 4 +
          (tokens > PIECE ? places * 2 * (size_t)dim * sizeof(Node) : 0);
 }
 
@@ -717,7 +767,11 @@ sv_status sv_embedding_backward(const void *dy, int64_t lddy, const void *ids, i
   unsigned *keys[2] = {(unsigned *)w, (unsigned *)(w + part)};
   int *tok[2] = {(int *)(w + 2 * part), (int *)(w + 3 * part)};
   unsigned *hist = (unsigned *)(w + 4 * part);
-  Node *nodes = (Node *)((char *)hist + (size_t)SORT_MAX_BLOCKS * SORT_RADIX * 4);
+  unsigned *sample = hist + SORT_MAX_BLOCKS * SORT_RADIX;
+  Node *nodes = (Node *)(sample + LDS_KEYS);
+  // few enough keys for LDS, and at least 16 apart: the rest is in one cache line
+  int sample_shift = tokens <= LDS_KEYS ? 0 : 4;
+  while (((tokens + ((int64_t)1 << sample_shift) - 1) >> sample_shift) > LDS_KEYS) ++sample_shift;
   int cur = 0;
   if (tokens > 0) {
     const SortPlan p = sort_plan(tokens, vocab);
@@ -731,7 +785,8 @@ sv_status sv_embedding_backward(const void *dy, int64_t lddy, const void *ids, i
         k_sort_hist<<<p.blocks, SORT_THREADS, 0, s>>>(ids, id_bytes, kin, tokens, vocab, padding, p.span, i * p.bits,
                                                       p.bits, hist);
         k_sort_scatter<<<p.blocks, SORT_THREADS, 0, s>>>(ids, id_bytes, kin, tin, tokens, vocab, padding, p.span,
-                                                         i * p.bits, p.bits, hist, keys[cur ^ 1], tok[cur ^ 1]);
+                                                         i * p.bits, p.bits, hist, keys[cur ^ 1], tok[cur ^ 1],
+                                                         i + 1 == p.passes ? sample : nullptr, sample_shift);
         cur ^= 1;
       }
     }
@@ -750,7 +805,8 @@ sv_status sv_embedding_backward(const void *dy, int64_t lddy, const void *ids, i
       per = per < 1 ? 1 : per > MAX_PER ? MAX_PER : per;
       const int64_t row_blocks = (units + per * G - 1) / (per * G);
       k_emb_grad<T, VE, L, U><<<(unsigned)(pieces + row_blocks), THREADS, 0, s>>>(
-          (const T *)dy, lddy, keys[cur], tok[cur], (int)tokens, vocab, dim, (int)tiles, scale, pieces, (int)per,
+          (const T *)dy, lddy, keys[cur], tok[cur], sample_shift ? sample : keys[cur], sample_shift, (int)tokens, vocab,
+          dim, (int)tiles, scale, pieces, (int)per,
           (T *)grad, ldg, nodes);
       if (pieces) {
         const int64_t blocks = places * tiles;
