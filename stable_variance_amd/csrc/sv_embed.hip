@@ -438,27 +438,36 @@ __device__ __forceinline__ void add_value(Node &a, float v) {
 // every 2^sample_shift-th key, which leaves a few steps in memory.
 constexpr int LDS_KEYS = 4096;
 
-// Adds the dy rows of the tokens at places [lo, hi) to the chunks of one
-// thread, FLIGHT tokens' loads at a time.
-constexpr int FLIGHT = 8;
+// Adds the dy rows of the tokens at places [lo, hi), hi > lo, to the chunks
+// of one thread, Q tokens' loads at a time.  Narrow tiles read the next
+// tokens' numbers meanwhile (wide ones lose more by the registers).
 template <class T, int VE, int L, int U>
 __device__ __forceinline__ void sum_run(const T *__restrict__ dy, int64_t lddy, const int *__restrict__ tok, int lo,
                                         int hi, const int64_t (&e)[U], Node (&a)[U][VE]) {
   using C = Cols<T, VE>;
+  constexpr int Q = L < 64 ? 16 : 8;  // short rows have little else in flight
 #pragma unroll
   for (int i = 0; i < U; ++i)
 #pragma unroll
     for (int j = 0; j < VE; ++j) a[i][j] = sv::zero_node();
-  for (int p = lo; p < hi; p += FLIGHT) {
-    typename C::Vec v[FLIGHT][U];
+  constexpr bool AHEAD = U == 1;
+  int t[Q];
+  const auto tokens_at = [&](int p) {
 #pragma unroll
-    for (int q = 0; q < FLIGHT; ++q) {
-      const int64_t t = tok[p + q < hi ? p + q : hi - 1];
+    for (int q = 0; q < Q; ++q) t[q] = tok[p + q < hi ? p + q : hi - 1];
+  };
+  if constexpr (AHEAD) tokens_at(lo);
+  for (int p = lo; p < hi; p += Q) {
+    typename C::Vec v[Q][U];
 #pragma unroll
-      for (int i = 0; i < U; ++i) v[q][i] = C::load(dy + t * lddy + e[i]);
+    for (int q = 0; q < Q; ++q) {
+      const int64_t row = AHEAD ? t[q] : tok[p + q < hi ? p + q : hi - 1];
+#pragma unroll
+      for (int i = 0; i < U; ++i) v[q][i] = C::load(dy + row * lddy + e[i]);
     }
+    if (AHEAD && p + Q < hi) tokens_at(p + Q);
 #pragma unroll
-    for (int q = 0; q < FLIGHT; ++q) {
+    for (int q = 0; q < Q; ++q) {
       if (p + q < hi) {
 #pragma unroll
         for (int i = 0; i < U; ++i)
@@ -776,7 +785,9 @@ sv_status sv_embedding_backward(const void *dy, int64_t lddy, const void *ids, i
   if (tokens > 0) {
     const SortPlan p = sort_plan(tokens, vocab);
     if (tokens <= SMALL_TOKENS) {
-      auto *k = tokens <= SORT_THREADS ? k_sort_small<1> : k_sort_small<SMALL_TOKENS / SORT_THREADS>;
+      auto *k = tokens <= SORT_THREADS       ? k_sort_small<1>
+                : tokens <= 2 * SORT_THREADS ? k_sort_small<2>
+                                             : k_sort_small<SMALL_TOKENS / SORT_THREADS>;
       k<<<1, SORT_THREADS, 0, s>>>(ids, id_bytes, (int)tokens, vocab, padding, p.passes, p.bits, keys[0], tok[0]);
     } else {
       for (int i = 0; i < p.passes; ++i) {
