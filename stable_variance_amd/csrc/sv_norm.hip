@@ -70,10 +70,16 @@ constexpr int tpb(int L) { return L <= 128 ? 256 : L; }
 // Rows that a group of L threads holds in registers, K chunks of 16 bytes per
 // thread: the row is read once, and the group's R - 1 neighbours in the
 // workgroup hold other rows.  The next row's loads are in flight while a row
-// is summed (PRE), and the parameters stay in registers across rows (WREG).
+// is summed (waited for before this row's stores, so that no store is ever
+// waited for), and up to 24 values' parameters stay in registers across rows.
 // Plain pairwise sums: with the shift and the second centring each is a sum
 // of values of the size of the spread, and 12 levels of rounding stay below
 // the result's own.
+// Bound by the read and the write: 16384 x 4096 bf16 51-54 us, 5.0-5.3 TB/s,
+// 4096 x 4096 float32 24-26 us; a large copy runs at 4.9-5.3 TB/s.  Next to
+// that is the vector unit (271 instructions per row and thread at 16 values,
+// about three quarters of the time).  Lengths that end inside a chunk: 43833
+// x 1531 bf16 64-67 us, 4.1 TB/s.
 template <class T, int L, int K, int FIT>
 __global__ __launch_bounds__(tpb(L)) void k_norm_rows(
     const T *__restrict__ x, int64_t rows, int n, int64_t ldx, const void *__restrict__ w,
@@ -201,7 +207,8 @@ bool with_tile(int64_t n, Fn &&fn) {
 
 // Rows of any length: a workgroup per row, each pass reads the row again (from
 // the cache where it fits).  Compensated sums, as a thread adds up a long run
-// of chunks one by one.
+// of chunks one by one.  335 x 200000 bf16: 151 us, 1.8 TB/s (a row's two later
+// passes and the parameters come from the cache).
 template <class T>
 __global__ __launch_bounds__(ROW_THREADS) void k_norm_any(const T *__restrict__ x, int64_t rows, int n, int64_t ldx,
                                                           const void *__restrict__ w, const void *__restrict__ bias,
@@ -248,7 +255,9 @@ __global__ __launch_bounds__(ROW_THREADS) void k_norm_any(const T *__restrict__ 
 // Threads of a workgroup of the backward pass: one workgroup per CU with as
 // many waves as the registers of E values allow, since every workgroup leaves
 // one partial column sum.
-constexpr int grad_tpb(int L, int E, int VE) { return (E <= 8 ? 1024 : E <= 16 && VE == 8 && L <= 256 ? 768 : 512) / L * L; }
+constexpr int grad_tpb(int L, int E, int VE) {
+  return (E <= 8 ? 1024 : E <= 16 && VE == 8 && L <= 256 ? 768 : 512) / L * L;
+}
 constexpr int GRAD_MAXL = 512, GRAD_MAXE = 24;
 constexpr int64_t GRAD_BLOCKS = 256;  // one workgroup per CU
 // Rows that one thread adds up in plain float32 for the columns' sums; the
@@ -256,12 +265,15 @@ constexpr int64_t GRAD_BLOCKS = 256;  // one workgroup per CU
 constexpr int64_t GRAD_RUN = 32;
 
 // The backward pass of rows that L threads hold (see k_norm_rows): x and dy
-// are read once, dx is stored non-temporal (16384 x 4096 bf16: 82 us plain, 76
-// so; the forward pass keeps plain stores, as its result is read next and
-// gains from the cache: 48 us plain, 53 non-temporal).  One cross-thread sum per row gives sum(d), sum(g) and
+// are read once.  One cross-thread sum per row gives sum(d), sum(g) and
 // sum(g d).  The column sums of the rows a group passes stay in registers;
 // at the end the workgroup's groups are added up through LDS into its row
-// of `part`, [gridDim.x][2][n] (part == nullptr: not asked for).
+// of `part`, [gridDim.x][2][n] (part == nullptr: not asked for).  dx is stored
+// non-temporal (16384 x 4096 bf16: 82 us plain, 76-80 so); the forward pass
+// keeps plain stores, whose result is read next and gains from the cache (48
+// us plain, 53 non-temporal).
+// Bound by the three streams: 16384 x 4096 bf16 80 us with the join, 5.1 TB/s;
+// the same size in float32 152 us, 5.3 TB/s.
 template <class T, int L, int K, int FIT>
 __global__ __launch_bounds__(grad_tpb(L, K * svr::Chunk<T>::VE, svr::Chunk<T>::VE)) void k_norm_grad(
     const T *__restrict__ dy, int64_t lddy, const T *__restrict__ x, int64_t ldx, int64_t rows, int n,
@@ -269,6 +281,8 @@ __global__ __launch_bounds__(grad_tpb(L, K * svr::Chunk<T>::VE, svr::Chunk<T>::V
     T *__restrict__ dx, int64_t lddx, float *__restrict__ part) {
   using Tile = svr::RowTile<T, L, K, FIT>;
   constexpr int E = Tile::E, VE = Tile::VE, TPB = grad_tpb(L, E, VE), R = TPB / L;
+  // the one tile whose registers do not also hold the next row
+  constexpr bool AHEAD = !(VE == 4 && E > 16 && L > 256 && FIT == svr::FIT_ANY);
   __shared__ float lds[2][3 * TPB / 64];
   __shared__ float cols[TPB * E];
   const int g = threadIdx.x / L, l0 = threadIdx.x % L;
@@ -298,10 +312,13 @@ __global__ __launch_bounds__(grad_tpb(L, K * svr::Chunk<T>::VE, svr::Chunk<T>::V
     Tile::load_rest(dy + rl * lddy, n, Tile::avail(rows, rl, lddy, n), l, gy);
     const float mu = m, rr = rs;
     rl = r + step < rows ? r + step : rows - 1;
-    Tile::load(x + rl * ldx, n, Tile::avail(rows, rl, ldx, n), l, rx);
-    Tile::load(dy + rl * lddy, n, Tile::avail(rows, rl, lddy, n), l, rg);
-    m = mean[rl];
-    rs = rstd[rl];
+    const auto load_next = [&] {
+      Tile::load(x + rl * ldx, n, Tile::avail(rows, rl, ldx, n), l, rx);
+      Tile::load(dy + rl * lddy, n, Tile::avail(rows, rl, lddy, n), l, rg);
+      m = mean[rl];
+      rs = rstd[rl];
+    };
+    if constexpr (AHEAD) load_next();
     Tile::set_rest(n, l, mu, d);
     Tile::set_rest(n, l, 0.0f, gy);
 #pragma unroll
@@ -321,6 +338,7 @@ __global__ __launch_bounds__(grad_tpb(L, K * svr::Chunk<T>::VE, svr::Chunk<T>::V
       }
       d[i] = rr * ((gy[i] * wv[i] - a) - xh * c);
     }
+    if constexpr (!AHEAD) load_next();
     Tile::arrived(rx, m);
     Tile::arrived(rg, rs);
     if (own && dx) {
@@ -346,8 +364,10 @@ __global__ __launch_bounds__(grad_tpb(L, K * svr::Chunk<T>::VE, svr::Chunk<T>::V
   }
 }
 
-// The rows' part of the backward pass for longer rows: dx and, for the column
-// sums, b.
+// The rows' part of the backward pass for longer rows (more than 12288 values,
+// whose column sums no workgroup's registers hold): dx and, for the column
+// sums, b.  With k_norm_dw_any x and dy are read from memory twice: 3355 x
+// 20000 bf16 178 us, 2.3 TB/s of the call's own bytes.
 template <class T>
 __global__ __launch_bounds__(ROW_THREADS) void k_norm_dx_any(
     const T *__restrict__ dy, int64_t lddy, const T *__restrict__ x, int64_t ldx, int64_t rows, int n,
@@ -615,9 +635,10 @@ sv_status sv_layer_norm_backward(const void *dy, int64_t lddy, const void *x, in
       svr::with_type(dtype, [&](auto t) {
         using T = decltype(t);
         with_tile<T, GRAD_MAXL, GRAD_MAXE>(n, [&](auto tl, auto tk, auto tf) {
-          constexpr int L = decltype(tl)::value, K = decltype(tk)::value, TPB = grad_tpb(L, K * svr::Chunk<T>::VE, svr::Chunk<T>::VE);
-          k_norm_grad<T, L, K, decltype(tf)::value><<<(unsigned)blocks, TPB, 0, s>>>(
-              (const T *)dy, lddy, (const T *)x, ldx, rows, (int)n, weight, param_dtype, mean, rstd, (T *)dx, lddx, part);
+          constexpr int L = decltype(tl)::value, K = decltype(tk)::value, VE = svr::Chunk<T>::VE;
+          k_norm_grad<T, L, K, decltype(tf)::value><<<(unsigned)blocks, grad_tpb(L, K * VE, VE), 0, s>>>(
+              (const T *)dy, lddy, (const T *)x, ldx, rows, (int)n, weight, param_dtype, mean, rstd, (T *)dx, lddx,
+              part);
         });
       });
     if (cols)

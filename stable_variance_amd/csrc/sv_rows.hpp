@@ -136,8 +136,8 @@ struct RowTile {
 
   // Starts the loads of the row; values past n hold anything.  The row's last
   // chunk may reach into the next row; where there is none, and for chunks
-  // outside the row, some other 16 bytes of the matrix are loaded (load_rest
-  // brings what is missing).  So every thread loads K chunks on every path
+  // outside the row, the row's first chunk is loaded instead (load_rest brings
+  // what is missing).  So every thread loads K chunks on every path
   // and the compiler can leave later loads in flight when it waits for these:
   // a load under a condition makes it wait for all.
   __device__ static __forceinline__ void load(const T *__restrict__ p, int n, int avail, int l, Vec (&raw)[K]) {
@@ -147,8 +147,7 @@ struct RowTile {
       int e = first(l, k);
       if (FIT != FIT_FULL) {
         const bool ok = FIT == FIT_ANY ? e < n && e + VE <= avail : e < n;
-        const int other = FIT == FIT_ANY && avail < VE ? avail - VE : 0;
-        e = ok ? e : other;
+        e = ok ? e : 0;  // avail >= n >= VE
       }
       __builtin_memcpy(&raw[k], p + e, 16);
     }

@@ -60,7 +60,7 @@ def _rows(t, rows, n):
 
 
 def _ptr(t):
-    return t.data_ptr() if t is not None and t.numel() else None
+    return None if t is None else t.data_ptr()
 
 
 def _scratch(nbytes, device, what):
@@ -98,8 +98,8 @@ def _norm_forward(x, weight, bias, eps, stats):
         y = torch.empty_like(x, memory_format=torch.contiguous_format)
         mean = rstd = None
         if stats:
-            mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
-            rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+            mean = x.new_empty(x.shape[:-1], dtype=torch.float32)
+            rstd = torch.empty_like(mean)
         _check(capi().sv_layer_norm(_ptr(x2), _CODES[x.dtype], rows, n, ldx, _ptr(w), _ptr(b), _CODES[pt], eps,
                                     _ptr(y), n, _ptr(mean), _ptr(rstd),
                                     _raw_stream(x.device.index)))

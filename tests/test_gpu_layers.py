@@ -661,6 +661,61 @@ def test_block_on_two_streams(dev):
             assert all(torch.equal(p, q) for p, q in zip(g, want[i]))
 
 
+def test_c_abi_row_strides_leave_the_gaps_alone(dev):
+    L = sv.capi()
+    st = torch.cuda.current_stream().cuda_stream
+    rows, vocab = 37, 50
+    for dtype, code in ((F32, 0), (BF16, 1), (F16, 2)):
+        for n, gap in ((5, 1), (64, 3), (100, 8), (1531, 5), (4096, 1), (20000, 7), (40001, 2)):
+            x, dy = hidden(rows, n, dtype, n), hidden(rows, n, dtype, n + 1)
+            w, b = params(n, F32, 1)
+            y, mean, rstd = sv.layer_norm(x, w, b, return_stats=True)
+            wide = torch.full((rows, n + gap), 7.0, dtype=dtype, device=dev)
+            assert L.sv_layer_norm(x.data_ptr(), code, rows, n, n, w.data_ptr(), b.data_ptr(), 0, 1e-5,
+                                   wide.data_ptr(), n + gap, None, None, st) == 0
+            assert torch.equal(wide[:, :n], y) and (wide[:, n:] == 7).all(), (n, gap)
+            want = sv.layer_norm_backward(dy, x, mean, rstd, w)[0]
+            wide.fill_(7.0)
+            assert L.sv_layer_norm_backward(dy.data_ptr(), n, x.data_ptr(), n, code, rows, n, w.data_ptr(), 0,
+                                            mean.data_ptr(), rstd.data_ptr(), wide.data_ptr(), n + gap, None, None,
+                                            None, 0, st) == 0
+            assert torch.equal(wide[:, :n], want) and (wide[:, n:] == 7).all(), (n, gap)
+            ids = ids_for("skewed", rows, vocab, torch.int64, n)
+            want = sv.embedding_backward(dy, ids, vocab)
+            grad = torch.full((vocab, n + gap), 7.0, dtype=dtype, device=dev)
+            need = L.sv_embedding_backward_workspace_size(rows, vocab, n, code)
+            ws = torch.empty(need, dtype=torch.uint8, device=dev)
+            assert L.sv_embedding_backward(dy.data_ptr(), n, ids.data_ptr(), 8, rows, code, vocab, n, 1.0, -1,
+                                           grad.data_ptr(), n + gap, ws.data_ptr(), need, st) == 0
+            assert torch.equal(grad[:, :n], want) and (grad[:, n:] == 7).all(), (n, gap)
+            assert L.sv_embedding(ids.data_ptr(), 8, rows, grad.data_ptr(), code, vocab, n, n + gap, 1.0,
+                                  wide.data_ptr(), n + gap, st) == 0
+            assert torch.equal(wide[:, :n], want[ids]) and (wide[:, n:] == 7).all(), (n, gap)
+
+
+def test_short_rows_are_independent_of_their_batch(dev):
+    for dtype in TYPES:
+        for n in range(1, 12):
+            x, dy = hidden(300, n, dtype, n), hidden(300, n, dtype, n + 20)
+            w, b = params(n, dtype, n)
+            y, mean, rstd = check_forward(x, w, b)
+            dx = check_backward(x, dy, w)[0]
+            for r in (0, 150, 299):
+                one = sv.layer_norm(x[r:r + 1], w, b, return_stats=True)
+                assert torch.equal(one[0], y[r:r + 1]) and torch.equal(one[1], mean[r:r + 1])
+                assert torch.equal(sv.layer_norm_backward(dy[r:r + 1], x[r:r + 1], one[1], one[2], w)[0], dx[r:r + 1])
+
+
+def test_many_equal_tokens(dev):
+    # runs of more than 64, 4096 and 64 * 64 pieces
+    for tokens in (2049, 2080, 4095, 4096, 4097, 131072, 131105, 270001):
+        dy = hidden(tokens, 8, F32, tokens)
+        check_lookup_grad(dy, ids_for("same", tokens, 9, torch.int32, 1), 9)
+        two = ids_for("same", tokens, 9, torch.int32, 1).clone()
+        two[::3] = 8
+        check_lookup_grad(dy, two, 9)
+
+
 # ---------------------------------------------------------------- refusals
 
 def test_refusals(dev):
