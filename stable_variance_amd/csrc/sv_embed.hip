@@ -64,7 +64,9 @@ constexpr int THREADS = 256;
 constexpr int64_t MAX_BLOCKS = (int64_t)1 << 23;  // 2^31 work-items, within HIP's grid limit
 
 // L threads per token and tile of L * U chunks; tile u belongs to token
-// u / tiles.  All U loads are in flight together.
+// u / tiles.  All U loads are in flight together.  Bound by memory: 32768 rows
+// of 4096 bf16 out of 64000 73-75 us, 4.9 TB/s of distinct rows and results
+// (5.5 TB/s moved, as a frequent row is fetched by every die's cache).
 template <class T, int VE, int L, int U>
 __global__ __launch_bounds__(THREADS) void k_emb_lookup(const void *__restrict__ ids, int id_bytes, int64_t units,
                                                         int tiles, const T *__restrict__ table, int64_t vocab,
@@ -120,6 +122,8 @@ void with_cols(int64_t dim, Fn &&fn) {
 
 // ---------------------------------------------------------------- sort
 
+// Bound by latency, not by bytes: 16384 tokens with two digits take 20 us in
+// four launches, 65536 with one digit 12 us, up to 1024 tokens 6 us in one.
 // Up to 64 workgroups of 1024 threads, each owning one run of `span` tokens
 // (a multiple of 1024).  A digit of `bits` <= 10 bits takes two launches: the
 // workgroups' histograms, then the scatter, where each workgroup finds its
@@ -491,6 +495,10 @@ __device__ __forceinline__ void store_roots(T *__restrict__ row, const int64_t (
   }
 }
 
+// Bound by memory where the table is large: 16384 tokens into 64000 x 4096 bf16
+// 139 us, 4.8 TB/s, of which writing the zeros of the other rows alone takes
+// about 90 (a fill runs at 6.9 TB/s, this at 5.8).  Bound by the chain of
+// loads (list, place, token, row) where it is small, about 10 us.
 // Blocks [0, pieces): a wave (or group of L threads) per block of PIECE
 // places and tile of L * U chunks.  Blocks behind: `per` <= L (row, tile)
 // units per group, rows of up to PIECE tokens.
