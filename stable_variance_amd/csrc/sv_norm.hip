@@ -168,16 +168,22 @@ __global__ __launch_bounds__(tpb(L)) void k_norm_rows(
   }
 }
 
-// Calls fn(L, K, FIT) (integral constants) with the smallest tile that holds
-// n values of T, of at most MAXL threads with MAXE values each; false
-// when none does.  The choice follows from n and the type alone.
-template <class T, int MAXL, int MAXE, class Fn>
+// The backward pass's tiles: up to 512 threads with 24 values (their registers
+// also hold the column sums), and 16 values for the shorter float32 rows
+// (446666 x 150: 205 us with 24 values, 170 with 16; bfloat16 is the other way
+// round, 43762 x 1531: 82 us with 24, 108 with 16).
+constexpr bool grad_tile(int L, int E, int VE) { return L <= 512 && E <= 24 && !(VE == 4 && E == 24 && L <= 64); }
+
+// Calls fn(L, K, FIT) (integral constants) with the smallest tile of the
+// forward (GRAD: backward) pass that holds n values of T; false when none
+// does.  The choice follows from n and the type alone.
+template <class T, bool GRAD, class Fn>
 bool with_tile(int64_t n, Fn &&fn) {
   constexpr int VE = svr::Chunk<T>::VE;
   if (n < 1) return false;
   const auto tile = [&](auto tl, auto tk) {
     constexpr int L = decltype(tl)::value, K = decltype(tk)::value;
-    if constexpr (L <= MAXL && K * VE <= MAXE) {
+    if constexpr (!GRAD || grad_tile(L, K * VE, VE)) {
       if (n > (int64_t)L * K * VE) return false;
       if constexpr (L == 1) {
         if (n < VE) {
@@ -258,7 +264,6 @@ __global__ __launch_bounds__(ROW_THREADS) void k_norm_any(const T *__restrict__ 
 constexpr int grad_tpb(int L, int E, int VE) {
   return (E <= 8 ? 1024 : E <= 16 && VE == 8 && L <= 256 ? 768 : 512) / L * L;
 }
-constexpr int GRAD_MAXL = 512, GRAD_MAXE = 24;
 constexpr int64_t GRAD_BLOCKS = 256;  // one workgroup per CU
 // Rows that one thread adds up in plain float32 for the columns' sums; the
 // workgroup's groups and then the workgroups are joined with compensation.
@@ -520,7 +525,7 @@ int64_t col_groups(int dtype, int64_t rows, int64_t n) {
 int64_t grad_blocks(int dtype, int64_t rows, int64_t n) {
   int64_t blocks = 0;
   svr::with_type(dtype, [&](auto t) {
-    with_tile<decltype(t), GRAD_MAXL, GRAD_MAXE>(n, [&](auto tl, auto tk, auto) {
+    with_tile<decltype(t), true>(n, [&](auto tl, auto tk, auto) {
       constexpr int L = decltype(tl)::value, E = decltype(tk)::value * svr::Chunk<decltype(t)>::VE;
       constexpr int64_t R = grad_tpb(L, E, svr::Chunk<decltype(t)>::VE) / L;
       const int64_t all = (rows + R - 1) / R;
@@ -574,7 +579,7 @@ sv_status sv_layer_norm(const void *x, int dtype, int64_t rows, int64_t n, int64
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   svr::with_type(dtype, [&](auto t) {
     using T = decltype(t);
-    const bool held = with_tile<T, 1024, 32>(n, [&](auto tl, auto tk, auto tf) {
+    const bool held = with_tile<T, false>(n, [&](auto tl, auto tk, auto tf) {
       constexpr int L = decltype(tl)::value, K = decltype(tk)::value, TPB = tpb(L), R = TPB / L;
       const int64_t blocks = (rows + R - 1) / R, most = 256 * (2048 / TPB);
       k_norm_rows<T, L, K, decltype(tf)::value><<<(unsigned)(blocks < most ? blocks : most), TPB, 0, s>>>(
@@ -634,7 +639,7 @@ sv_status sv_layer_norm_backward(const void *dy, int64_t lddy, const void *x, in
     if (rows > 0)
       svr::with_type(dtype, [&](auto t) {
         using T = decltype(t);
-        with_tile<T, GRAD_MAXL, GRAD_MAXE>(n, [&](auto tl, auto tk, auto tf) {
+        with_tile<T, true>(n, [&](auto tl, auto tk, auto tf) {
           constexpr int L = decltype(tl)::value, K = decltype(tk)::value, VE = svr::Chunk<T>::VE;
           k_norm_grad<T, L, K, decltype(tf)::value><<<(unsigned)blocks, grad_tpb(L, K * VE, VE), 0, s>>>(
               (const T *)dy, lddy, (const T *)x, ldx, rows, (int)n, weight, param_dtype, mean, rstd, (T *)dx, lddx,
