@@ -89,7 +89,7 @@ __global__ __launch_bounds__(tpb(L)) void k_norm_rows(
   constexpr int E = Tile::E, TPB = tpb(L), R = TPB / L;
   constexpr bool HOLD = E <= 24;
   __shared__ float lds_a[TPB / 64], lds_b[2 * TPB / 64];
-  const int g = threadIdx.x / L, l0 = threadIdx.x % L;
+  const int g = svr::group_of<L>(), l0 = threadIdx.x % L;
   const float inv_n = 1.0f / (float)n;
   constexpr int VE = Tile::VE;
   float wv[HOLD ? E : 1], bv[HOLD ? E : 1];
@@ -168,11 +168,13 @@ __global__ __launch_bounds__(tpb(L)) void k_norm_rows(
   }
 }
 
-// The backward pass's tiles: up to 512 threads with 24 values (their registers
-// also hold the column sums), and 16 values for the shorter float32 rows
+// The backward pass's tiles: up to 24 values on 512 threads and 16 on 1024 (their
+// registers also hold the column sums), and 16 values for the shorter float32 rows
 // (446666 x 150: 205 us with 24 values, 170 with 16; bfloat16 is the other way
 // round, 43762 x 1531: 82 us with 24, 108 with 16).
-constexpr bool grad_tile(int L, int E, int VE) { return L <= 512 && E <= 24 && !(VE == 4 && E == 24 && L <= 64); }
+constexpr bool grad_tile(int L, int E, int VE) {
+  return (L <= 512 ? E <= 24 : E <= 16) && !(VE == 4 && E == 24 && L <= 64);
+}
 
 // Calls fn(L, K, FIT) (integral constants) with the smallest tile of the
 // forward (GRAD: backward) pass that holds n values of T; false when none
@@ -191,9 +193,11 @@ bool with_tile(int64_t n, Fn &&fn) {
           return true;
         }
       }
+      constexpr bool WHOLE = GRAD && L > 512;  // whole chunks only: no register is left for the others
+      if (WHOLE && n % VE != 0) return false;
       if (n == (int64_t)L * K * VE) fn(tl, tk, std::integral_constant<int, svr::FIT_FULL>{});
       else if (n % VE == 0) fn(tl, tk, std::integral_constant<int, svr::FIT_CHUNKS>{});
-      else fn(tl, tk, std::integral_constant<int, svr::FIT_ANY>{});
+      else if constexpr (!WHOLE) fn(tl, tk, std::integral_constant<int, svr::FIT_ANY>{});
       return true;
     }
     return false;
@@ -262,7 +266,7 @@ __global__ __launch_bounds__(ROW_THREADS) void k_norm_any(const T *__restrict__ 
 // many waves as the registers of E values allow, since every workgroup leaves
 // one partial column sum.
 constexpr int grad_tpb(int L, int E, int VE) {
-  return (E <= 8 ? 1024 : E <= 16 && VE == 8 && L <= 256 ? 768 : 512) / L * L;
+  return (E <= 8 || L > 512 ? 1024 : E <= 16 && VE == 8 && L <= 256 ? 768 : 512) / L * L;
 }
 constexpr int64_t GRAD_BLOCKS = 256;  // one workgroup per CU
 // Rows that one thread adds up in plain float32 for the columns' sums; the
@@ -286,15 +290,24 @@ __global__ __launch_bounds__(grad_tpb(L, K * svr::Chunk<T>::VE, svr::Chunk<T>::V
     T *__restrict__ dx, int64_t lddx, float *__restrict__ part) {
   using Tile = svr::RowTile<T, L, K, FIT>;
   constexpr int E = Tile::E, VE = Tile::VE, TPB = grad_tpb(L, E, VE), R = TPB / L;
-  // the one tile whose registers do not also hold the next row
-  constexpr bool AHEAD = !(VE == 4 && E > 16 && L > 256 && FIT == svr::FIT_ANY);
+  // 1024 threads leave 128 registers each: the weight then waits in LDS (a
+  // thread reads back what it wrote) and the next row is loaded after this one
+  constexpr bool FEW = L > 512;
+  constexpr bool AHEAD = !FEW && !(VE == 4 && E > 16 && L > 256 && FIT == svr::FIT_ANY);
+  __shared__ float wlds[FEW ? TPB * E : 1];
   __shared__ float lds[2][3 * TPB / 64];
   __shared__ float cols[TPB * E];
-  const int g = threadIdx.x / L, l0 = threadIdx.x % L;
+  const int g = svr::group_of<L>(), l0 = threadIdx.x % L;
   const float inv_n = 1.0f / (float)n;
-  float wv[E], aw[E], ab[E];
+  float wv[FEW ? VE : E], aw[E], ab[E];
 #pragma unroll
-  for (int k = 0; k < K; ++k) svr::load_param<T, L>(w, pt, n, l0, k, 1.0f, wv + k * VE);
+  for (int k = 0; k < K; ++k) {
+    svr::load_param<T, L>(w, pt, n, l0, k, 1.0f, wv + (FEW ? 0 : k * VE));
+    if constexpr (FEW) {
+#pragma unroll
+      for (int i = 0; i < VE; ++i) wlds[Tile::first(l0, k) + i] = wv[i];
+    }
+  }
 #pragma unroll
   for (int i = 0; i < E; ++i) aw[i] = ab[i] = 0.0f;
   const int64_t step = (int64_t)gridDim.x * R;
@@ -304,8 +317,10 @@ __global__ __launch_bounds__(grad_tpb(L, K * svr::Chunk<T>::VE, svr::Chunk<T>::V
   Tile::load(x + rl * ldx, n, Tile::avail(rows, rl, ldx, n), l0, rx);
   Tile::load(dy + rl * lddy, n, Tile::avail(rows, rl, lddy, n), l0, rg);
   float m = mean[rl], rs = rstd[rl];
-  Tile::arrived(rx, m);
-  Tile::arrived(rg, rs);
+  if constexpr (AHEAD) {
+    Tile::arrived(rx, m);
+    Tile::arrived(rg, rs);
+  }
   int turn = 0;
   for (int64_t r0 = (int64_t)blockIdx.x * R; r0 < rows; r0 += step, r += step, turn ^= 1) {
     int l = l0;  // opaque, as in k_norm_rows
@@ -328,28 +343,40 @@ __global__ __launch_bounds__(grad_tpb(L, K * svr::Chunk<T>::VE, svr::Chunk<T>::V
     Tile::set_rest(n, l, 0.0f, gy);
 #pragma unroll
     for (int i = 0; i < E; ++i) d[i] = d[i] - mu;
-    float s[3] = {Tile::sum(n, l, [&](int i) { return d[i]; }), Tile::sum(n, l, [&](int i) { return gy[i] * wv[i]; }),
-                  Tile::sum(n, l, [&](int i) { return (gy[i] * wv[i]) * d[i]; })};
+    const auto weight = [&](int i) { return FEW ? wlds[Tile::first(l, i / VE) + i % VE] : wv[FEW ? 0 : i]; };
+    float s[3] = {Tile::sum(n, l, [&](int i) { return d[i]; }),
+                  Tile::sum(n, l, [&](int i) { return gy[i] * weight(i); }),
+                  Tile::sum(n, l, [&](int i) { return (gy[i] * weight(i)) * d[i]; })};
     svr::group_sum<L, 3>(s, lds[turn]);
     const float b = s[0] * inv_n, a = s[1] * inv_n;
     const float c = rr * ((s[2] - b * s[1]) * inv_n);
     const bool own = R == 1 || r < rows;
+    // keeps the compiler from spreading a step's values over the next
+    const auto step_done = [] {
+      if constexpr (FEW) __builtin_amdgcn_sched_barrier(0);
+    };
+    step_done();
 #pragma unroll
     for (int i = 0; i < E; ++i) {
+      if (i % VE == 0) step_done();
       const float xh = (d[i] - b) * rr;
       if (own) {
         aw[i] = aw[i] + gy[i] * xh;
         ab[i] = ab[i] + gy[i];
       }
-      d[i] = rr * ((gy[i] * wv[i] - a) - xh * c);
+      d[i] = rr * ((gy[i] * weight(i) - a) - xh * c);
     }
-    if constexpr (!AHEAD) load_next();
-    Tile::arrived(rx, m);
-    Tile::arrived(rg, rs);
+    step_done();
+    if constexpr (AHEAD) {
+      Tile::arrived(rx, m);
+      Tile::arrived(rg, rs);
+    }
     if (own && dx) {
 #pragma unroll
       for (int k = 0; k < K; ++k) Tile::template store_chunk<true>(dx + r * lddx, n, l, k, d);
     }
+    step_done();
+    if constexpr (!AHEAD) load_next();
   }
   if (!part) return;
   for (int which = 0; which < 2; ++which) {
@@ -369,9 +396,9 @@ __global__ __launch_bounds__(grad_tpb(L, K * svr::Chunk<T>::VE, svr::Chunk<T>::V
   }
 }
 
-// The rows' part of the backward pass for longer rows (more than 12288 values,
-// whose column sums no workgroup's registers hold): dx and, for the column
-// sums, b.  With k_norm_dw_any x and dy are read from memory twice: 3355 x
+// The rows' part of the backward pass for longer rows, whose column sums no
+// workgroup's registers hold (more than 16384 values, or more than 12288 that
+// end inside a chunk): dx and, for the column sums, b.  With k_norm_dw_any x and dy are read from memory twice: 3355 x
 // 20000 bf16 178 us, 2.3 TB/s of the call's own bytes.
 template <class T>
 __global__ __launch_bounds__(ROW_THREADS) void k_norm_dx_any(

@@ -284,6 +284,14 @@ __device__ __forceinline__ void load_param(const void *__restrict__ p, int dtype
   }
 }
 
+// The group of L threads that this thread belongs to, in a scalar register
+// where a group is whole waves (and the row's addresses with it).
+template <int L>
+__device__ __forceinline__ int group_of() {
+  const int g = threadIdx.x / L;
+  return L >= 64 ? __builtin_amdgcn_readfirstlane(g) : g;
+}
+
 // Sums of NV values per thread over each group of L consecutive threads, in
 // a fixed order (lanes pairwise, then the group's waves pairwise); every
 // thread of the group gets them.  L > 64 takes a barrier and `lds`, which

@@ -88,7 +88,7 @@ def check_forward(x, w, b, eps=1e-5):
 
 
 LENGTHS = [1, 2, 3, 5, 7, 8, 9, 31, 63, 64, 65, 100, 127, 128, 129, 255, 256, 257, 300, 511, 512, 513, 768, 1000, 1023,
-           1024, 1025, 1531, 2047, 2048, 2050, 4095, 4096, 4104, 5000, 8191, 8192, 8200, 12288, 16384, 16385, 20001,
+           1024, 1025, 1531, 2047, 2048, 2050, 4095, 4096, 4104, 5000, 8191, 8192, 8200, 12288, 12290, 14000, 16384, 16385, 20001,
            32768, 32776, 33000, 70001]
 
 
