@@ -14,6 +14,10 @@
  *                     centring by the plain tree of the shifted values,
  *                     compensated trees of d and d^2, two-term correction
  *                     and ddof rescale.
+ *   sv_layer_norm, sv_embedding and their backward calls
+ *                     the layer norm of rows on those statistics, the lookup
+ *                     of a table's rows, and the gradients of both, in
+ *                     float32 and 16-bit types.
  *
  * Arithmetic: IEEE binary32, round to nearest even, every operation rounded
  * on its own (no FMA contraction, no reassociation, subnormals kept).

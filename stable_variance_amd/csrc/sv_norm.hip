@@ -77,8 +77,8 @@ constexpr int tpb(int L) { return L <= 128 ? 256 : L; }
 // the result's own.
 // Bound by the read and the write: 16384 x 4096 bf16 51-54 us, 5.0-5.3 TB/s,
 // 4096 x 4096 float32 24-26 us; a large copy runs at 4.9-5.3 TB/s.  Next to
-// that is the vector unit (271 instructions per row and thread at 16 values,
-// about three quarters of the time).  Lengths that end inside a chunk: 43833
+// that is the vector unit (about 265 instructions per row and wave at 16 values
+// a thread, three quarters of the time).  Lengths that end inside a chunk: 43833
 // x 1531 bf16 64-67 us, 4.1 TB/s.
 template <class T, int L, int K, int FIT>
 __global__ __launch_bounds__(tpb(L)) void k_norm_rows(

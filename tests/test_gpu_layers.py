@@ -88,8 +88,8 @@ def check_forward(x, w, b, eps=1e-5):
 
 
 LENGTHS = [1, 2, 3, 5, 7, 8, 9, 31, 63, 64, 65, 100, 127, 128, 129, 255, 256, 257, 300, 511, 512, 513, 768, 1000, 1023,
-           1024, 1025, 1531, 2047, 2048, 2050, 4095, 4096, 4104, 5000, 8191, 8192, 8200, 12288, 12290, 14000, 16384, 16385, 20001,
-           32768, 32776, 33000, 70001]
+           1024, 1025, 1531, 2047, 2048, 2050, 4095, 4096, 4104, 5000, 8191, 8192, 8200, 12288, 12290, 14000, 16384, 16385,
+           20001, 32768, 32776, 33000, 70001]
 
 
 @pytest.mark.parametrize("dtype", TYPES, ids=IDS.get)
@@ -405,6 +405,33 @@ def test_lookup_strides_and_bad_ids(dev):
     assert sv.embedding(ids, torch.empty(0, 6, device=dev)).isnan().all()
     assert sv.embedding(torch.empty(0, 4, dtype=torch.int32, device=dev), table).shape == (0, 4, 97)
     assert sv.embedding(ids, torch.empty(9, 0, device=dev)).shape == (2, 3, 0)
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=IDS.get)
+def test_lookup_and_gradient_of_special_values(dev, dtype):
+    # signed zeros, subnormals, the largest values, Inf and NaN: rounded as
+    # the host rounds them
+    tiny, big = torch.finfo(dtype).tiny, torch.finfo(dtype).max
+    v = torch.tensor([0.0, -0.0, tiny, -tiny, tiny / 4, -tiny / 8, tiny * 0.75, big, -big, float("inf"), float("-inf"),
+                      float("nan"), 1.0, 1.0 + torch.finfo(dtype).eps, 3.0e-41, -1.2e-39], dtype=torch.float64)
+    table = v.to(dtype).repeat(3, 5)  # 80 values a row: whole chunks
+    ids = torch.arange(3)
+    for cols in (80, 77, 3):
+        t = table[:, :cols].contiguous()
+        for scale in (1.0, 0.5, 3.0, -1.0):
+            want = (t.float() * scale).to(dtype)
+            got = sv.embedding(ids.to(dev), t.to(dev), scale=scale).cpu()
+            assert torch.equal(got.isnan(), want.isnan())
+            keep = ~want.isnan()
+            assert torch.equal(got[keep], want[keep]) and torch.equal(got[keep].signbit(), want[keep].signbit())
+            grad = sv.embedding_backward(t.to(dev), ids.to(dev), 3, scale=scale).cpu()
+            assert torch.equal(grad.isnan(), want.isnan()) and torch.equal(grad[keep], want[keep])
+    # sums that overflow the type, or meet Inf of both signs
+    dy = torch.tensor([[big, big, float("inf"), -big]] * 2 + [[0.0, -big, float("-inf"), 1.0]], dtype=torch.float64)
+    got = sv.embedding_backward(dy.to(dtype).to(dev), torch.zeros(3, dtype=torch.int32, device=dev), 1).cpu()[0]
+    assert got[0] == float("inf") and got[2].isnan() and got[3] == float("-inf")
+    # big + big - big: float32 holds the sum in float16's range only
+    assert got[1] == (big if dtype == F16 else float("inf"))
 
 
 def test_lookup_beyond_2_31_values(dev):
