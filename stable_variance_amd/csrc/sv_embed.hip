@@ -368,10 +368,9 @@ __global__ __launch_bounds__(SORT_THREADS) void k_sort_small(const void *__restr
 // column and a second launch joins a row's nodes in order.
 //
 // Pieces are found by block of PIECE places of the sorted list: a run longer
-// than PIECE has exactly one piece starting in every block that it crosses,
-// and a block meets at most two such runs, the one that holds its first
-// place and the one that holds its last.  Their nodes go to slots 2 b and
-// 2 b + 1 of block b.
+// than PIECE has at most one piece starting in a block, and a block meets at
+// most two such runs, the one that holds its first place and the one that
+// holds its last.  Their nodes go to slots 2 b and 2 b + 1 of block b.
 constexpr int PIECE = 32;
 constexpr int64_t WIDE_ROWS = 16384;  // rows and pieces from which tiles are wide
 
