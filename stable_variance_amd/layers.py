@@ -5,7 +5,9 @@ are float32, bfloat16 or float16 on one HIP device; every call runs on the
 current stream of that device, allocates its outputs and scratch from torch's
 allocator (so it can be captured in a HIP graph) and does not synchronise.
 ``layer_norm`` and ``embedding`` take part in autograd: their gradients are
-``layer_norm_backward`` and ``embedding_backward``.
+``layer_norm_backward`` and ``embedding_backward``, which are plain calls
+without a derivative of their own.  There is no forward-mode derivative: a
+dual tensor is refused (``NotImplementedError``).
 """
 from __future__ import annotations
 
@@ -14,6 +16,7 @@ import ctypes
 import math
 
 import torch
+from torch.autograd import forward_ad
 
 from . import SvError, _check, capi
 
@@ -34,6 +37,16 @@ def _tensor(t, name, dtypes):
         raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
     if not t.is_cuda:
         raise ValueError(f"{name} must be on a HIP device, got {t.device}")
+
+
+def _no_tangents(*tensors):
+    """Refuses dual tensors: no forward-mode derivative is computed here, and a
+    result without its tangent would pass for a constant."""
+    if getattr(forward_ad, "_current_level", 0) < 0:  # not within a dual level: one comparison
+        return
+    for t in tensors:
+        if isinstance(t, torch.Tensor) and forward_ad.unpack_dual(t).tangent is not None:
+            raise NotImplementedError("the layer norm and the embedding have no forward-mode derivative")
 
 
 def _same_device(ref, t, name):
@@ -138,6 +151,7 @@ def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, return_stats: bool 
     other rows.
     """
     _tensor(x, "x", tuple(_CODES))
+    _no_tangents(x, weight, bias)
     eps = float(eps)
     if torch.is_grad_enabled() and (x.requires_grad or (weight is not None and weight.requires_grad)
                                     or (bias is not None and bias.requires_grad)):
@@ -148,6 +162,7 @@ def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, return_stats: bool 
 
 
 def _norm_backward(dy, x, mean, rstd, weight, need_x, need_w, need_b, param_dtype):
+    _no_tangents(dy, x, mean, rstd, weight)
     rows, n = _shape_2d(x, "x")
     w = _param(weight, "weight", x, n) if weight is not None else None
     dy2, lddy = _rows(dy, rows, n)
@@ -222,6 +237,7 @@ def _lookup(ids, table, scale):
 
 
 def _lookup_backward(dy, ids, vocab, scale, padding):
+    _no_tangents(dy)
     dim = dy.shape[-1]
     ids1 = ids.contiguous()
     tokens = ids1.numel()
@@ -260,6 +276,7 @@ def embedding(ids, table, scale: float = 1.0, padding_idx=None):
     concerns the gradient: its tokens take no part in it.
     """
     _tensor(table, "table", tuple(_CODES))
+    _no_tangents(table)
     _tensor(ids, "ids", (torch.int32, torch.int64))
     _same_device(table, ids, "ids")
     if table.dim() != 2:
