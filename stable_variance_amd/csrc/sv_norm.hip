@@ -505,15 +505,16 @@ __device__ __forceinline__ Node node_of(Node v) { return v; }
 
 // Joins the partial sums part[groups][2][n] of 64 columns of dw (blocks [0,
 // ctiles)) or dbias (blocks [ctiles, 2 ctiles)): wave i adds up groups i,
-// i + 16, .. in order, then the waves are joined pairwise.
+// i + 16, .. in order, then the waves are joined pairwise.  The launch starts
+// at block b0.
 constexpr int JOIN_WAVES = 16;
 template <class P>
-__global__ __launch_bounds__(64 * JOIN_WAVES) void k_norm_join(const P *__restrict__ part, int groups, int n,
+__global__ __launch_bounds__(64 * JOIN_WAVES) void k_norm_join(const P *__restrict__ part, int groups, int n, int b0,
                                                                int ctiles, void *__restrict__ dw,
                                                                void *__restrict__ db, int pt) {
   __shared__ Node lds[JOIN_WAVES][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int which = blockIdx.x >= (unsigned)ctiles, j = ((int)blockIdx.x - which * ctiles) * 64 + lane;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, block = b0 + (int)blockIdx.x;
+  const int which = block >= ctiles, j = (block - which * ctiles) * 64 + lane;
   void *out = which ? db : dw;
   if (!out) return;
   Node s = sv::zero_node();
@@ -529,6 +530,17 @@ __global__ __launch_bounds__(64 * JOIN_WAVES) void k_norm_join(const P *__restri
     for (int i = 0; i < JOIN_WAVES; ++i) t[i] = lds[i][lane];
     svr::store_as(out, j, pt, sv::root_value(sv::node_tree<0, JOIN_WAVES, JOIN_WAVES>(t)));
   }
+}
+
+// k_norm_join over all columns, in launches within HIP's limit (the longest
+// rows have 2^22 tiles for dw and dbias, 2^32 work-items).
+template <class P>
+void join_columns(const P *part, int64_t groups, int64_t n, void *dw, void *db, int pt, hipStream_t s) {
+  const int64_t ctiles = (n + 63) / 64;
+  svh::in_batches(2 * ctiles, 1, 64 * JOIN_WAVES, [&](int64_t b0, int64_t blocks) {
+    k_norm_join<P><<<(unsigned)blocks, 64 * JOIN_WAVES, 0, s>>>(part, (int)groups, (int)n, (int)b0, (int)ctiles, dw,
+                                                                db, pt);
+  });
 }
 
 // Workgroups of k_norm_dw_any across a row.
@@ -659,7 +671,6 @@ sv_status sv_layer_norm_backward(const void *dy, int64_t lddy, const void *x, in
   if ((st = check_device()) != SV_OK) return st;
   (void)hipGetLastError();
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-  const int ctiles = (int)((n + 63) / 64);
   const int64_t blocks = grad_blocks(dtype, rows, n);
   if (blocks) {
     float *part = cols ? reinterpret_cast<float *>(workspace) : nullptr;
@@ -673,9 +684,7 @@ sv_status sv_layer_norm_backward(const void *dy, int64_t lddy, const void *x, in
               part);
         });
       });
-    if (cols)
-      k_norm_join<float><<<(unsigned)(2 * ctiles), 64 * JOIN_WAVES, 0, s>>>(part, rows > 0 ? (int)blocks : 0, (int)n,
-                                                                           ctiles, dweight, dbias, param_dtype);
+    if (cols) join_columns(part, rows > 0 ? blocks : 0, n, dweight, dbias, param_dtype, s);
     return check_launch(who);
   }
   float *off = cols ? reinterpret_cast<float *>(workspace) : nullptr;
@@ -691,9 +700,7 @@ sv_status sv_layer_norm_backward(const void *dy, int64_t lddy, const void *x, in
       k_norm_dw_any<T><<<(unsigned)(groups * wtiles), 64 * COL_WAVES, 0, s>>>(g, lddy, xx, ldx, rows, (int)n, mean,
                                                                               rstd, off, groups, wtiles, part);
   });
-  if (cols)
-    k_norm_join<Node><<<(unsigned)(2 * ctiles), 64 * JOIN_WAVES, 0, s>>>(part, groups, (int)n, ctiles, dweight,
-                                                                         dbias, param_dtype);
+  if (cols) join_columns(part, groups, n, dweight, dbias, param_dtype, s);
   return check_launch(who);
 }
 

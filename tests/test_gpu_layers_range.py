@@ -1,0 +1,43 @@
+"""Layer norm and embedding on the GPU over the ranges that the header gives:
+launches cut into batches, the longest rows, the smallest eps, many rows for
+every tile, wide tables with long runs of tokens.  Bounds as in
+test_gpu_layers.py, from whose checks in float64 these are built."""
+import pytest
+import torch
+
+import stable_variance_amd as sv
+from test_gpu_layers import (BF16, F16, F32, IDS, TYPES, check_backward, check_forward, check_lookup_grad,  # noqa: F401
+                             dev, hidden, ids_for, params)
+
+pytestmark = pytest.mark.gpu
+
+
+# ---------------------------------------------------------------- launches
+
+@pytest.mark.parametrize("dtype", TYPES, ids=IDS.get)
+def test_column_join_in_batches_gives_the_same_bits(dev, dtype):
+    for rows, n in ((40, 200), (3, 4096), (700, 1531), (5, 20001)):
+        w, _ = params(n, dtype, n)
+        x, dy = hidden(rows, n, dtype, n), hidden(rows, n, dtype, n + 1)
+        _, mean, rstd = sv.layer_norm(x, w, return_stats=True)
+        want = sv.layer_norm_backward(dy, x, mean, rstd, w)
+        for items in (1024, 5000):
+            sv.set_tuning("launch_items", items)
+            try:
+                got = sv.layer_norm_backward(dy, x, mean, rstd, w)
+                only = sv.layer_norm_backward(dy, x, mean, rstd, w, weight_grad=False)
+            finally:
+                sv.set_tuning("reset", 0)
+            assert all(torch.equal(p, q) for p, q in zip(got, want)), (rows, n, items)
+            assert torch.equal(only[2], want[2])
+
+
+def test_longest_rows(dev):
+    # 2 * 2^21 tiles of 64 columns: more than one launch of the column join
+    for n in ((1 << 27) - 63, 1 << 27):
+        print("longest", n, flush=True)
+        x, dy = hidden(2, n, BF16, 1), hidden(2, n, BF16, 2)
+        w, _ = params(n, F32, 3)
+        dx, dw, db = check_backward(x, dy, w)
+        del x, dy, dx, dw, db
+        torch.cuda.empty_cache()
