@@ -364,7 +364,8 @@ sv_status sv_adn_sum_f32(const float *x, int64_t n, int fold, float *out, void *
  * x + r * ldx values):
  *   m1 = x_0 + Sum(x_i - x_0) / n,  d_i = x_i - m1,  b = Sum(d_i) / n
  *   var = max(Sum(d_i^2) / n - b^2, 0),  mean = m1 + b,
- *   rstd = 1 / sqrt(var + eps)            (rounded from double)
+ *   rstd = 1 / sqrt(var + eps)            (rounded from double, at most the
+ *                                          largest float32 when eps > 0)
  *   y_i = ((d_i - b) * rstd) * weight_i + bias_i
  * the shift, centring and two-term correction of sv_variance_f32 with ddof
  * 0; the sums are pairwise or compensated sums whose order is fixed by n and

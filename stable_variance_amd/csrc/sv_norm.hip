@@ -38,13 +38,16 @@ constexpr int64_t COL_MAX_GROUPS = 512;
 
 // 1 / sqrt(v) in double (one Newton step from the hardware's estimate, about
 // 2^-46), so that the float32 value is the rounded one; 0, Inf and NaN as
-// the estimate gives them.
+// the estimate gives them.  Above float32's range (var = 0 and eps below
+// 8.6e-78) it is the largest finite value: with Inf, equal values would give
+// 0 * Inf = NaN in place of the bias, and NaN gradients.
 __device__ __forceinline__ float rstd_of(float var, double eps) {
   const double v = (double)var + eps;
   const double r = __builtin_amdgcn_rsq(v);
   const double e = 1.0 - v * r * r;
   const double s = r + 0.5 * r * e;
-  return (float)(__builtin_isfinite(e) ? s : r);
+  const float f = (float)(__builtin_isfinite(e) ? s : r);
+  return v > 0.0 && f > __FLT_MAX__ ? __FLT_MAX__ : f;
 }
 
 // Sum of one node per thread over the workgroup, in a fixed order; every

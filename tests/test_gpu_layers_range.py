@@ -41,3 +41,23 @@ def test_longest_rows(dev):
         dx, dw, db = check_backward(x, dy, w)
         del x, dy, dx, dw, db
         torch.cuda.empty_cache()
+
+
+# ---------------------------------------------------------------- eps
+
+@pytest.mark.parametrize("dtype", TYPES, ids=IDS.get)
+def test_equal_values_give_the_bias_for_the_smallest_eps(dev, dtype):
+    # 1 / sqrt(eps) is beyond float32: no 0 * Inf, and no NaN in the gradients
+    biggest = torch.finfo(F32).max
+    for n in (1, 6, 128, 1531, 4096, 14000, 40000):
+        x = torch.tensor([0.0, 1.0, -3.25], device=dev).to(dtype)[:, None].repeat(1, n)
+        w, b = params(n, dtype, n)
+        for eps in (8.6e-78, 1e-80, 1e-200, 5e-324):
+            y, mean, rstd = sv.layer_norm(x, w, b, eps=eps, return_stats=True)
+            assert torch.equal(y, b.expand_as(y)), (n, eps)
+            assert torch.equal(mean, x[:, 0].float()) and (rstd == biggest).all(), (n, eps)
+            dx, dw, db = sv.layer_norm_backward(torch.ones_like(x), x, mean, rstd, w)
+            assert not dx.isnan().any() and (dw == 0).all() and (db == 3).all(), (n, eps)
+        # in range: rounded as ever
+        _, _, rstd = sv.layer_norm(x, w, b, eps=8.7e-78, return_stats=True)
+        assert torch.equal(rstd, torch.full_like(rstd, float(torch.tensor(8.7e-78, dtype=torch.float64) ** -0.5)))
