@@ -59,9 +59,16 @@ def _on(device):
     return _HERE if device.index == torch.cuda.current_device() else torch.cuda.device(device)
 
 
+def _stored(t):
+    """t with the values that its memory holds (torch negates some views as it
+    reads them: imaginary parts of conjugates)."""
+    return t.detach().resolve_neg() if t.is_neg() else t
+
+
 def _rows(t, rows, n):
     """t as [rows, n] with contiguous rows (a view where its strides allow
     one, else a copy), and its row stride."""
+    t = _stored(t)
     if t.is_contiguous():
         return t, n
     t = t.detach().reshape(rows, n)
@@ -98,7 +105,7 @@ def _param(t, name, x, n, dtype=None):
         raise ValueError(f"{name} must have shape ({n},), got {tuple(t.shape)}")
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"weight and bias must have one type, got {dtype} and {t.dtype}")
-    return t.contiguous()
+    return _stored(t).contiguous()
 
 
 def _norm_forward(x, weight, bias, eps, stats):
@@ -167,7 +174,7 @@ def _norm_backward(dy, x, mean, rstd, weight, need_x, need_w, need_b, param_dtyp
     w = _param(weight, "weight", x, n) if weight is not None else None
     dy2, lddy = _rows(dy, rows, n)
     x2, ldx = _rows(x, rows, n)
-    mean, rstd = mean.contiguous(), rstd.contiguous()
+    mean, rstd = _stored(mean).contiguous(), _stored(rstd).contiguous()
     L = capi()
     with _on(x.device):
         dx = torch.empty_like(x, memory_format=torch.contiguous_format) if need_x else None
@@ -226,7 +233,7 @@ def _padding(padding_idx, vocab):
 
 def _lookup(ids, table, scale):
     vocab, dim = table.shape
-    ids1 = ids.contiguous()
+    ids1 = _stored(ids).contiguous()
     t2, ldt = _rows(table, vocab, dim)
     with _on(table.device):
         out = torch.empty(ids.shape + (dim,), dtype=table.dtype, device=table.device)
@@ -239,7 +246,7 @@ def _lookup(ids, table, scale):
 def _lookup_backward(dy, ids, vocab, scale, padding):
     _no_tangents(dy)
     dim = dy.shape[-1]
-    ids1 = ids.contiguous()
+    ids1 = _stored(ids).contiguous()
     tokens = ids1.numel()
     dy2, lddy = _rows(dy, tokens, dim)
     L = capi()

@@ -117,3 +117,28 @@ def test_a_tangent_of_the_result_gradient_is_refused(lib, op):
         with pytest.raises(NotImplementedError):
             y.backward(dy)
     assert v[leaf].grad is None
+
+
+def negated(t, dense):
+    """A view of -t that torch negates as it is read (the negative bit set)."""
+    if dense:
+        return torch._neg_view(-t)
+    z = torch.complex(torch.zeros_like(t), -t)  # an imaginary part: strides of 2
+    return z.conj().imag
+
+
+@pytest.mark.parametrize("dense", [True, False])
+@pytest.mark.parametrize("op", CALLS)
+def test_the_negative_bit_reaches_the_library_as_values(lib, op, dense):
+    names, call = CALLS[op]
+    for cols in (6, 1):  # single columns are taken with any stride
+        v = {k: t[..., :cols].contiguous() if t.dim() == 2 or k in ("w", "b") else t for k, t in inputs().items()}
+        call(v)
+        for name in names:
+            w = dict(v)
+            w[name] = negated(v[name], dense)
+            assert w[name].is_neg() and torch.equal(w[name], v[name])
+            call(w)
+        for got in lib.calls[1:]:
+            assert all(p is q is None or torch.equal(p, q) for p, q in zip(got[1:], lib.calls[0][1:])), cols
+        lib.calls.clear()
