@@ -160,8 +160,9 @@ def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, return_stats: bool 
     _tensor(x, "x", tuple(_CODES))
     _no_tangents(x, weight, bias)
     eps = float(eps)
-    if torch.is_grad_enabled() and (x.requires_grad or (weight is not None and weight.requires_grad)
-                                    or (bias is not None and bias.requires_grad)):
+    # what is no tensor is refused where the parameters are checked
+    if torch.is_grad_enabled() and (x.requires_grad or getattr(weight, "requires_grad", False)
+                                    or getattr(bias, "requires_grad", False)):
         y, mean, rstd = _LayerNorm.apply(x, weight, bias, eps)
     else:
         y, mean, rstd = _norm_forward(x, weight, bias, eps, return_stats)

@@ -142,3 +142,13 @@ def test_the_negative_bit_reaches_the_library_as_values(lib, op, dense):
         for got in lib.calls[1:]:
             assert all(p is q is None or torch.equal(p, q) for p, q in zip(got[1:], lib.calls[0][1:])), cols
         lib.calls.clear()
+
+
+def test_arguments_that_are_no_tensors(lib):
+    v = inputs()
+    for requires_grad in (False, True):
+        v["x"].requires_grad_(requires_grad)
+        for w, b in (([1.0] * 6, None), (v["w"], 0.5), (None, [0.0] * 6), (1.0, v["b"])):
+            with pytest.raises(TypeError):
+                sv.layer_norm(v["x"], w, b)
+    assert lib.calls == []
