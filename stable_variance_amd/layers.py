@@ -14,6 +14,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import math
+import operator
 
 import torch
 from torch.autograd import forward_ad
@@ -227,9 +228,10 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, *, weight_grad: bool = T
 def _padding(padding_idx, vocab):
     if padding_idx is None:
         return -1
-    if not 0 <= int(padding_idx) < vocab:
+    padding_idx = operator.index(padding_idx)
+    if not 0 <= padding_idx < vocab:
         raise ValueError(f"padding_idx {padding_idx} outside [0, {vocab})")
-    return int(padding_idx)
+    return padding_idx
 
 
 def _lookup(ids, table, scale):
@@ -306,7 +308,7 @@ def embedding_backward(dy, ids, num_embeddings: int, scale: float = 1.0, padding
     _same_device(dy, ids, "ids")
     if dy.dim() != ids.dim() + 1 or dy.shape[:-1] != ids.shape:
         raise ValueError(f"dy must have shape {tuple(ids.shape)} + (dim,), got {tuple(dy.shape)}")
-    num_embeddings = int(num_embeddings)
+    num_embeddings = operator.index(num_embeddings)
     if num_embeddings < 0:
         raise ValueError("num_embeddings must be >= 0")
     return _lookup_backward(dy, ids, num_embeddings, float(scale), _padding(padding_idx, num_embeddings))

@@ -152,3 +152,19 @@ def test_arguments_that_are_no_tensors(lib):
             with pytest.raises(TypeError):
                 sv.layer_norm(v["x"], w, b)
     assert lib.calls == []
+
+
+def test_numbers_of_rows_are_whole(lib):
+    # 1.5 was taken for 1
+    v = inputs()
+    for bad in (1.5, 2.0, "3", torch.tensor(1.0)):
+        with pytest.raises(TypeError):
+            sv.embedding(v["ids"], v["table"], padding_idx=bad)
+        with pytest.raises(TypeError):
+            sv.embedding_backward(v["dy"], v["ids"], 5, padding_idx=bad)
+        with pytest.raises(TypeError):
+            sv.embedding_backward(v["dy"], v["ids"], bad)
+    assert lib.calls == []
+    for good in (4, torch.tensor(4), True):
+        sv.embedding(v["ids"], v["table"], padding_idx=good)
+        sv.embedding_backward(v["dy"], v["ids"], 5, padding_idx=good)
