@@ -61,3 +61,59 @@ def test_equal_values_give_the_bias_for_the_smallest_eps(dev, dtype):
         # in range: rounded as ever
         _, _, rstd = sv.layer_norm(x, w, b, eps=8.7e-78, return_stats=True)
         assert torch.equal(rstd, torch.full_like(rstd, float(torch.tensor(8.7e-78, dtype=torch.float64) ** -0.5)))
+
+
+# ---------------------------------------------------------------- many rows
+
+# Lengths that fill a tile, end on a 16-byte chunk and end inside one, for
+# every tile of 128 threads and more.
+LONG = [2048, 1600, 1999, 4096, 3000, 2050, 6144, 5000, 5003, 8192, 7000, 7001, 12288, 10000, 10001, 16384, 14000, 13001,
+        32768, 20000, 20001]
+
+
+def pick(rows):
+    """Rows of the first, a middle and the last round of the launch."""
+    return sorted({0, 1, rows // 3, rows // 2, rows - 300, rows - 2, rows - 1})
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=IDS.get)
+def test_norm_many_long_rows(dev, dtype):
+    # every group of threads takes at least two rows, most three: the launch
+    # has 2048 workgroups of 256 threads (two rows of 128 threads each), 1024
+    # of 512 and 512 of 1024
+    for i, n in enumerate(LONG):
+        rows = 77 + (8192 if n <= 2048 else 4096 if n <= 6144 else 2048 if n <= 12288 else 1024)
+        print("many rows", IDS[dtype], rows, n, flush=True)
+        w, b = params(n, dtype if i % 2 else F32, i)
+        x = hidden(rows, n, dtype, i)
+        whole = check_forward(x, w, b)
+        for r in pick(rows):
+            one = sv.layer_norm(x[r:r + 1], w, b, return_stats=True)
+            assert all(torch.equal(p[r:r + 1], q) for p, q in zip(whole, one)), (n, r)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=IDS.get)
+def test_norm_grad_many_long_rows(dev, dtype):
+    # 256 workgroups of 1 to 6 groups: at least three rows per group
+    for i, n in enumerate(LONG):
+        rows = 3200 if n <= 2048 else 1700 if n <= 4096 else 1150 if n <= 6144 else 800
+        print("many rows", IDS[dtype], rows, n, flush=True)
+        w, _ = params(n, dtype if i % 2 else F32, i)
+        x, dy = hidden(rows, n, dtype, i), hidden(rows, n, dtype, 900 + i)
+        whole = check_backward(x, dy, w)
+        for r in pick(rows):
+            one = check_backward(x[r:r + 1], dy[r:r + 1], w)
+            assert torch.equal(one[0], whole[0][r:r + 1]), (n, r)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=IDS.get)
+def test_norm_grad_more_than_one_round_of_workgroups(dev, dtype):
+    # more than 32 rows per group of 256 workgroups: 512 of them
+    for rows, n in ((8300, 8192), (17000, 5003), (50000, 1600), (800000, 128)):
+        print("rounds", IDS[dtype], rows, n, flush=True)
+        w, _ = params(n, F32, n)
+        x, dy = hidden(rows, n, dtype, 1), hidden(rows, n, dtype, 2)
+        whole = check_backward(x, dy, w)
+        for r in pick(rows):
+            one = check_backward(x[r:r + 1], dy[r:r + 1], w)
+            assert torch.equal(one[0], whole[0][r:r + 1]), (n, r)
