@@ -117,3 +117,30 @@ def test_norm_grad_more_than_one_round_of_workgroups(dev, dtype):
         for r in pick(rows):
             one = check_backward(x[r:r + 1], dy[r:r + 1], w)
             assert torch.equal(one[0], whole[0][r:r + 1]), (n, r)
+
+
+# ---------------------------------------------------------------- wide tables
+
+@pytest.mark.parametrize("dtype", TYPES, ids=IDS.get)
+def test_lookup_grad_wide_tiles_with_long_runs(dev, dtype):
+    # tables and token lists from which two chunks per thread are taken, rows
+    # that end inside the second chunk, take several tiles, or one; runs of
+    # one token to all of them, in lists searched whole and by samples
+    for i, (tokens, vocab, dim, kind) in enumerate((
+            (9000, 17000, 1100, "skewed"), (4096, 17000, 1025, "skewed"), (5000, 20000, 600, "same"),
+            (4097, 16400, 2049, "same"), (3000, 16384, 520, "skewed"), (70000, 16384, 1000, "skewed"),
+            (40000, 20000, 4096, "skewed"), (600000, 300, 513, "skewed"))):
+        print("wide", IDS[dtype], tokens, vocab, dim, kind, flush=True)
+        ids = ids_for(kind, tokens, vocab, torch.int64 if i % 2 else torch.int32, i)
+        dy = hidden(tokens, dim, dtype, i)
+        scale = (1.0, 0.37)[i % 2]
+        whole = check_lookup_grad(dy, ids, vocab, scale=scale)
+        assert torch.equal(whole, sv.embedding_backward(dy, ids, vocab, scale=scale))
+        # the same tokens alone, into a table that takes the narrow tiles
+        rows = [0, 1, 2, 40, 199] if kind == "skewed" else [vocab // 2]
+        for v in rows:
+            at = (ids == v).nonzero()[:, 0]
+            if len(at) == 0 or len(at) > 500000:
+                continue
+            alone = sv.embedding_backward(dy[at], torch.zeros_like(at), 1, scale=scale)
+            assert torch.equal(alone[0], whole[v]), (tokens, vocab, dim, v, len(at))
