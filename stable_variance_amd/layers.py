@@ -24,6 +24,7 @@ from . import SvError, _check, capi
 __all__ = ["layer_norm", "layer_norm_backward", "embedding", "embedding_backward"]
 
 _CODES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+_TYPES = tuple(_CODES)
 _UNSUPPORTED = ctypes.c_size_t(-1).value
 _HERE = contextlib.nullcontext()
 # the raw stream handle without a Stream object, where torch has the call
@@ -43,15 +44,13 @@ def _tensor(t, name, dtypes):
 def _no_tangents(*tensors):
     """Refuses dual tensors: no forward-mode derivative is computed here, and a
     result without its tangent would pass for a constant."""
-    if getattr(forward_ad, "_current_level", 0) < 0:  # not within a dual level: one comparison
-        return
-    for t in tensors:
-        if isinstance(t, torch.Tensor) and forward_ad.unpack_dual(t).tangent is not None:
-            raise NotImplementedError("the layer norm and the embedding have no forward-mode derivative")
+    if forward_ad._current_level >= 0 and any(
+            isinstance(t, torch.Tensor) and forward_ad.unpack_dual(t).tangent is not None for t in tensors):
+        raise NotImplementedError("the layer norm and the embedding have no forward-mode derivative")
 
 
 def _same_device(ref, t, name):
-    if t.device != ref.device:
+    if t.get_device() != ref.get_device():  # both on HIP devices, as _tensor has checked
         raise ValueError(f"{name} is on {t.device}, the other tensors on {ref.device}")
 
 
@@ -61,15 +60,16 @@ def _on(device):
 
 
 def _stored(t):
-    """t with the values that its memory holds (torch negates some views as it
-    reads them: imaginary parts of conjugates)."""
-    return t.detach().resolve_neg() if t.is_neg() else t
+    """t's values, contiguous in memory.  Torch negates some views as it reads
+    them (imaginary parts of conjugates): their memory holds the opposite."""
+    return (t.detach().resolve_neg() if t.is_neg() else t).contiguous()
 
 
 def _rows(t, rows, n):
     """t as [rows, n] with contiguous rows (a view where its strides allow
     one, else a copy), and its row stride."""
-    t = _stored(t)
+    if t.is_neg():
+        t = _stored(t)
     if t.is_contiguous():
         return t, n
     t = t.detach().reshape(rows, n)
@@ -106,7 +106,7 @@ def _param(t, name, x, n, dtype=None):
         raise ValueError(f"{name} must have shape ({n},), got {tuple(t.shape)}")
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"weight and bias must have one type, got {dtype} and {t.dtype}")
-    return _stored(t).contiguous()
+    return _stored(t)
 
 
 def _norm_forward(x, weight, bias, eps, stats):
@@ -158,7 +158,7 @@ def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, return_stats: bool 
     is not contiguous is copied first.  A row's result does not depend on the
     other rows.
     """
-    _tensor(x, "x", tuple(_CODES))
+    _tensor(x, "x", _TYPES)
     _no_tangents(x, weight, bias)
     eps = float(eps)
     # what is no tensor is refused where the parameters are checked
@@ -176,7 +176,7 @@ def _norm_backward(dy, x, mean, rstd, weight, need_x, need_w, need_b, param_dtyp
     w = _param(weight, "weight", x, n) if weight is not None else None
     dy2, lddy = _rows(dy, rows, n)
     x2, ldx = _rows(x, rows, n)
-    mean, rstd = _stored(mean).contiguous(), _stored(rstd).contiguous()
+    mean, rstd = _stored(mean), _stored(rstd)
     L = capi()
     with _on(x.device):
         dx = torch.empty_like(x, memory_format=torch.contiguous_format) if need_x else None
@@ -200,7 +200,7 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, *, weight_grad: bool = T
     type or float32, when there is no weight; float32 by default) and are
     None where not asked for.
     """
-    _tensor(x, "x", tuple(_CODES))
+    _tensor(x, "x", _TYPES)
     _tensor(dy, "dy", (x.dtype,))
     _same_device(x, dy, "dy")
     if dy.shape != x.shape:
@@ -236,7 +236,7 @@ def _padding(padding_idx, vocab):
 
 def _lookup(ids, table, scale):
     vocab, dim = table.shape
-    ids1 = _stored(ids).contiguous()
+    ids1 = _stored(ids)
     t2, ldt = _rows(table, vocab, dim)
     with _on(table.device):
         out = torch.empty(ids.shape + (dim,), dtype=table.dtype, device=table.device)
@@ -249,7 +249,7 @@ def _lookup(ids, table, scale):
 def _lookup_backward(dy, ids, vocab, scale, padding):
     _no_tangents(dy)
     dim = dy.shape[-1]
-    ids1 = _stored(ids).contiguous()
+    ids1 = _stored(ids)
     tokens = ids1.numel()
     dy2, lddy = _rows(dy, tokens, dim)
     L = capi()
@@ -285,7 +285,7 @@ def embedding(ids, table, scale: float = 1.0, padding_idx=None):
     An id outside ``[0, vocab)`` gives a row of NaN.  ``padding_idx`` only
     concerns the gradient: its tokens take no part in it.
     """
-    _tensor(table, "table", tuple(_CODES))
+    _tensor(table, "table", _TYPES)
     _no_tangents(table)
     _tensor(ids, "ids", (torch.int32, torch.int64))
     _same_device(table, ids, "ids")
@@ -303,7 +303,7 @@ def embedding_backward(dy, ids, num_embeddings: int, scale: float = 1.0, padding
     each row the compensated sum of its tokens' gradients in token order,
     times ``scale``.  Ids outside the table and ``padding_idx`` take no part.
     """
-    _tensor(dy, "dy", tuple(_CODES))
+    _tensor(dy, "dy", _TYPES)
     _tensor(ids, "ids", (torch.int32, torch.int64))
     _same_device(dy, ids, "ids")
     if dy.dim() != ids.dim() + 1 or dy.shape[:-1] != ids.shape:
