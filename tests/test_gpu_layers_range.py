@@ -1,13 +1,14 @@
 """Layer norm and embedding on the GPU over the ranges that the header gives:
 launches cut into batches, the longest rows, the smallest eps, many rows for
-every tile, wide tables with long runs of tokens.  Bounds as in
+every tile, wide tables with long runs of tokens, many tokens, autograd in a
+graph.  Bounds as in
 test_gpu_layers.py, from whose checks in float64 these are built."""
 import pytest
 import torch
 
 import stable_variance_amd as sv
 from test_gpu_layers import (BF16, F16, F32, IDS, TYPES, check_backward, check_forward, check_lookup_grad,  # noqa: F401
-                             dev, hidden, ids_for, params)
+                             dev, gen, hidden, ids_for, params)
 
 pytestmark = pytest.mark.gpu
 
@@ -144,3 +145,63 @@ def test_lookup_grad_wide_tiles_with_long_runs(dev, dtype):
                 continue
             alone = sv.embedding_backward(dy[at], torch.zeros_like(at), 1, scale=scale)
             assert torch.equal(alone[0], whole[v]), (tokens, vocab, dim, v, len(at))
+
+
+# ---------------------------------------------------------------- many tokens
+
+def test_lookup_of_more_tokens_than_one_grid(dev):
+    # 2^23 workgroups of 32 tokens each, then a second round
+    tokens, vocab = (1 << 28) + 77, 1000
+    table = torch.arange(vocab, device=dev, dtype=F32).to(F16)[:, None]
+    ids = torch.arange(tokens, device=dev, dtype=torch.int32).remainder_(vocab)
+    out = sv.embedding(ids, table, scale=2.0)
+    assert out.shape == (tokens, 1) and torch.equal(out[:, 0], ids.to(F16) * 2)
+
+
+def test_lookup_grad_of_many_tokens(dev):
+    tokens, vocab = (1 << 27) + 77, 5
+    ids = torch.arange(tokens, device=dev, dtype=torch.int32).remainder_(vocab)
+    # whole numbers of mean 0: every partial sum (tens of thousands at most) is
+    # exact in float32, and so is the result
+    dy = torch.randint(-2, 3, (tokens, 2), generator=gen(1), device=dev).float()
+    got = sv.embedding_backward(dy, ids, vocab, scale=0.5)
+    want = torch.stack([dy[v::vocab].double().sum(0) for v in range(vocab)])
+    assert torch.equal(got.double(), want * 0.5)
+
+
+# ---------------------------------------------------------------- autograd in a graph
+
+def test_block_with_autograd_captured_and_replayed(dev):
+    vocab, dim, tokens = 300, 520, 700
+    table = torch.randn(vocab, dim, generator=gen(1), device=dev).to(BF16)
+    w, b = params(dim, F32, 1)
+    ids = ids_for("skewed", tokens, vocab, torch.int64, 1).clone()
+    dy = hidden(tokens, dim, BF16, 2).clone()
+
+    def explicit():
+        x = sv.embedding(ids, table, scale=3.0)
+        y, mean, rstd = sv.layer_norm(x, w, b, return_stats=True)
+        dx, dw, db = sv.layer_norm_backward(dy, x, mean, rstd, w)
+        return y, sv.embedding_backward(dx, ids, vocab, scale=3.0), dw, db
+
+    data = [(ids_for(k, tokens, vocab, torch.int64, 10 + i), hidden(tokens, dim, BF16, 20 + i))
+            for i, k in enumerate(("skewed", "same", "uniform"))]
+    explicit()
+    torch.cuda.synchronize()
+    # leaves of their own that no eager graph holds
+    leaves = [t.clone().requires_grad_() for t in (table, w, b)]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=torch.cuda.Stream()):
+        y = sv.layer_norm(sv.embedding(ids, leaves[0], scale=3.0), leaves[1], leaves[2])
+        out = (y.detach(), *torch.autograd.grad(y, leaves, dy))
+    del y
+    for rep in range(6):
+        ids.copy_(data[rep % 3][0])
+        dy.copy_(data[rep % 3][1])
+        want = explicit()
+        torch.cuda.synchronize()
+        for t in out:
+            t.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, q) for p, q in zip(out, want)), rep
