@@ -381,8 +381,10 @@ sv_status sv_adn_sum_f32(const float *x, int64_t n, int fold, float *out, void *
  *   y            [rows, n] of dtype, row stride ldy; must not overlap x
  *   mean, rstd   rows float32 values each, each may be NULL
  * Row strides are in values, at least n; x and y need only the alignment of
- * their type (16-byte aligned rows are the fastest).  n == 0 gives mean =
- * rstd = NaN.  n <= 2^27, rows * n <= 2^36 and strides * rows <= 2^40, else
+ * their type (16-byte aligned rows are the fastest).  Where a stride is above
+ * n, up to 15 bytes behind a row of x that another row follows may be read
+ * (and are not used): they must be readable.  Nothing is written between rows.
+ * n == 0 gives mean = rstd = NaN.  n <= 2^27, rows * n <= 2^36 and strides * rows <= 2^40, else
  * SV_ERR_UNSUPPORTED.  No workspace.
  */
 sv_status sv_layer_norm(const void *x, int dtype, int64_t rows, int64_t n, int64_t ldx, const void *weight,
@@ -400,7 +402,8 @@ sv_status sv_layer_norm(const void *x, int dtype, int64_t rows, int64_t n, int64
  *   dbias_j = sum over the rows of dy_j
  * Every sum's order is fixed by the shape and dtype: the same bits on every
  * run, no atomics.
- *   dtype          SV_DTYPE_* of dy, x and dx; strides as for sv_layer_norm
+ *   dtype          SV_DTYPE_* of dy, x and dx; strides as for sv_layer_norm,
+ *                  and what lies between the rows of dy and x likewise
  *   weight         may be NULL (then 1)
  *   param_dtype    type of weight, dweight and dbias: dtype or SV_DTYPE_F32
  *   dx, dweight, dbias  each may be NULL: that gradient is not computed.

@@ -64,9 +64,11 @@ constexpr int THREADS = 256;
 constexpr int64_t MAX_BLOCKS = (int64_t)1 << 23;  // 2^31 work-items, within HIP's grid limit
 
 // L threads per token and tile of L * U chunks; tile u belongs to token
-// u / tiles.  All U loads are in flight together.  Bound by memory: 32768 rows
-// of 4096 bf16 out of 64000 73-75 us, 4.9 TB/s of distinct rows and results
-// (5.5 TB/s moved, as a frequent row is fetched by every die's cache).
+// u / tiles.  All U loads are in flight together.  Bound by memory: a call for
+// 32768 rows of 4096 bf16 out of 64000 takes 72-75 us among others, 4.8-5.0
+// TB/s of distinct rows and results (358 MB).  Under the profiler the kernel
+// takes 77-79 us and moves 441 MB, 5.6 TB/s: a frequent row is fetched by every
+// die's cache.
 template <class T, int VE, int L, int U>
 __global__ __launch_bounds__(THREADS) void k_emb_lookup(const void *__restrict__ ids, int id_bytes, int64_t units,
                                                         int tiles, const T *__restrict__ table, int64_t vocab,
@@ -833,8 +835,18 @@ sv_status sv_embedding_backward(const void *dy, int64_t lddy, const void *ids, i
       }
     };
     // Wide tiles write longer runs of a row; narrow ones give more groups work.
-    // 64000 rows x 4096 bf16: 164 us wide, 193 narrow; 256 rows of 65536 tokens
-    // x 512 float32: 65 us wide, 58 narrow.
+    // Wide and narrow, us a call (dim > 64 chunks; shorter rows have one form):
+    //   16384 tokens into 64000 rows x 4096 bf16   164  193
+    //   65536                64000 x 4096          287  318    float32  490  535
+    //   65536                20000 x 4096          224  228             345  367
+    //   65536                 2000 x 4096          187  187             278  299
+    //    5000                20000 x 4096           64   62              93   91
+    //   65536                64000 x 1024          117  106             162  161
+    //   65536                  300 x 1024           82   62              92   89
+    //   65536                64000 x  600          100   86             136  123
+    // So the rule, which looks at the rows and pieces alone, fits rows of 4096
+    // values; for shorter rows of large tables narrow tiles would be up to a
+    // fifth faster, and for float32 rows of 4096 wide ones by 6% in small tables.
     if (vocab + tokens / PIECE >= WIDE_ROWS) with_cols<T, 2 * (16 / (int)sizeof(T))>(dim, go);
     else with_cols<T, 16 / (int)sizeof(T)>(dim, go);
   });

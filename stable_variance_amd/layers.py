@@ -8,6 +8,10 @@ allocator (so it can be captured in a HIP graph) and does not synchronise.
 ``layer_norm_backward`` and ``embedding_backward``, which are plain calls
 without a derivative of their own.  There is no forward-mode derivative: a
 dual tensor is refused (``NotImplementedError``).
+
+A captured backward pass is subject to torch's own rule: no eager graph of
+the same leaves may be alive while it is captured, as their gradients would
+then be ordered against the eager graph's stream, outside the capture.
 """
 from __future__ import annotations
 
@@ -283,7 +287,9 @@ def embedding(ids, table, scale: float = 1.0, padding_idx=None):
     ``[vocab, dim]``, rounded once: shape ``ids.shape + (dim,)``.
 
     An id outside ``[0, vocab)`` gives a row of NaN.  ``padding_idx`` only
-    concerns the gradient: its tokens take no part in it.
+    concerns the gradient: its tokens take no part in it.  The table's rows may
+    be strided; a table whose last dimension is not contiguous (a transposed
+    one) is copied whole in every call.
     """
     _tensor(table, "table", _TYPES)
     _no_tangents(table)
