@@ -18,6 +18,13 @@
  *                     the layer norm of rows on those statistics, the lookup
  *                     of a table's rows, and the gradients of both, in
  *                     float32 and 16-bit types.
+ *   sv_rms_norm, sv_rms_norm_fp8, sv_rms_norm_backward
+ *                     the root-mean-square norm of rows with the residual's
+ *                     addition, its output in the rows' type or in 8 bits
+ *                     with scales, and its gradient.
+ *   sv_grad_norm, sv_clip_grad_norm
+ *                     the norm of many tensors as one vector, and their
+ *                     scaling down to a largest norm.
  *
  * Arithmetic: IEEE binary32, round to nearest even, every operation rounded
  * on its own (no FMA contraction, no reassociation, subnormals kept).
@@ -452,6 +459,117 @@ size_t sv_embedding_backward_workspace_size(int64_t tokens, int64_t vocab, int64
 sv_status sv_embedding_backward(const void *dy, int64_t lddy, const void *ids, int id_bytes, int64_t tokens,
                                 int dtype, int64_t vocab, int64_t dim, float scale, int64_t padding, void *grad,
                                 int64_t ldg, void *workspace, size_t workspace_bytes, void *stream);
+
+/* 8-bit types of an output (OCP): largest values 448 and 57344. */
+#define SV_DTYPE_E4M3 3 /* e4m3fn: Inf has no code */
+#define SV_DTYPE_E5M2 4
+
+/*
+ * Root-mean-square norm of each row of the [rows, n] matrix x, with the
+ * residual's addition:
+ *   h_i = x_i + residual_i     rounded to sum_dtype and written to sum
+ *                              (h = x when residual and sum are NULL)
+ *   rstd = 1 / sqrt(Sum(h_i^2) / n + eps)   (rounded once, at most the
+ *                              largest float32 when eps > 0)
+ *   y_i = (h_i * rstd) * weight_i           float32, rounded once to dtype
+ * The squares are exact and summed in double, so no finite row overflows or
+ * underflows there; rstd itself is a float32 (a root mean square above 2^126
+ * makes it subnormal, one below 2^-128 with eps = 0 is beyond it).  A row of
+ * zeros gives 0 when eps > 0 (eps = 0 divides zero by zero: NaN).  An Inf in a row gives NaN in its place and
+ * 0 in the others, a NaN makes the whole row NaN; no other row changes.  A
+ * row's outputs have the same bits on every run and do not depend on the
+ * other rows.
+ *   dtype        SV_DTYPE_F32, BF16 or F16: of x and y
+ *   sum_dtype    of residual and sum: dtype or SV_DTYPE_F32 (dtype when they
+ *                are NULL; both are given or neither)
+ *   weight       n values of param_dtype (dtype or SV_DTYPE_F32), or NULL (1)
+ *   eps          >= 0 and finite
+ *   y, sum       [rows, n], row strides ldy and ldsum; must not overlap each
+ *                other, x or residual
+ *   rstd         rows float32 values, may be NULL
+ * Strides, alignment and limits as for sv_layer_norm, and what lies behind
+ * the rows of x and residual likewise.  n == 0 gives rstd = NaN.
+ */
+sv_status sv_rms_norm(const void *x, int64_t ldx, const void *residual, int64_t ldr, int dtype, int sum_dtype,
+                      int64_t rows, int64_t n, const void *weight, int param_dtype, double eps, void *y, int64_t ldy,
+                      void *sum, int64_t ldsum, float *rstd, void *stream);
+
+/*
+ * The same norm with its output in 8 bits: for each block of `block` values
+ * of a row (128; the row's last block may be shorter) or, with block == 0,
+ * for each whole row, with y_i in float32 as above:
+ *   scale = max(max|y_i| / M, 2^-126),  M = 448 (E4M3) or 57344 (E5M2)
+ *   q_i = y_i * (1 / scale), cut to [-M, M] and rounded once to out_dtype
+ * so that q_i * scale stands for y_i.  An Inf among a block's values makes its
+ * scale Inf, its own q NaN and the others 0; a NaN makes both NaN.
+ *   q          [rows, n] bytes, row stride ldq
+ *   scale      [rows, ceil(n / 128)] float32 values without gaps, or [rows]
+ * The other arguments as above.
+ */
+sv_status sv_rms_norm_fp8(const void *x, int64_t ldx, const void *residual, int64_t ldr, int dtype, int sum_dtype,
+                          int64_t rows, int64_t n, const void *weight, int param_dtype, double eps, int out_dtype,
+                          int64_t block, void *q, int64_t ldq, float *scale, void *sum, int64_t ldsum, float *rstd,
+                          void *stream);
+
+/*
+ * Gradient of the root-mean-square norm at the rows h that were normed (x, or
+ * the written sum), for the gradient dy of y and, with a residual, the
+ * gradient dsum of the written sum.  With g_i = dy_i * weight_i and
+ * xhat_i = h_i * rstd:
+ *   dh_i = rstd * (g_i - xhat_i * c) + dsum_i,  c = Sum(g_i xhat_i) / n
+ *   dweight_j = sum over the rows of dy_j * xhat_j
+ * dh is the gradient of x and of the residual alike.  Every sum's order is
+ * fixed by the shape and the types: the same bits on every run, no atomics.
+ *   dtype          of dy and dx
+ *   sum_dtype      of h, dsum and dh: dtype or SV_DTYPE_F32
+ *   dsum           may be NULL (then 0)
+ *   dh, dx         the gradient rounded to sum_dtype and to dtype; each may be
+ *                  NULL.  They must not overlap each other, dy, h or dsum
+ *   weight, param_dtype  as for sv_layer_norm_backward
+ *   dweight        may be NULL: not computed.  With rows == 0 it is set to zero
+ *   workspace      sv_rms_norm_backward_workspace_size(...) bytes, 256-byte
+ *                  aligned scratch (no initialisation, nothing kept); may be
+ *                  NULL when dweight is NULL or the size is 0
+ * Limits as for sv_layer_norm ((size_t)-1 beyond them).
+ */
+size_t sv_rms_norm_backward_workspace_size(int64_t rows, int64_t n, int dtype, int sum_dtype);
+sv_status sv_rms_norm_backward(const void *dy, int64_t lddy, const void *h, int64_t ldh, const void *dsum,
+                               int64_t lddsum, int dtype, int sum_dtype, int64_t rows, int64_t n, const void *weight,
+                               int param_dtype, const float *rstd, void *dh, int64_t lddh, void *dx, int64_t lddx,
+                               void *dweight, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * norm = sqrt(Sum of g^2) over all values of `count` tensors (a model's
+ * gradients), squares and sums in double, rounded once to float32: 0 for no
+ * values, Inf for an Inf among them, NaN for a NaN.  The order of the sum
+ * follows from the sizes and types in their order: the same bits on every run.
+ *   tensors    host array of device addresses (aligned to their types)
+ *   sizes      host array: values of each, 0 <= size <= 2^40
+ *   dtypes     host array: SV_DTYPE_F32, BF16 or F16 of each
+ *   norm       one float32
+ *   workspace  sv_grad_norm_workspace_size(sizes, dtypes, count) bytes,
+ *              256-byte aligned scratch (no initialisation, nothing kept)
+ * The host arrays are read before the call returns.  count <= 2^20.
+ */
+size_t sv_grad_norm_workspace_size(const int64_t *sizes, const int *dtypes, int64_t count);
+sv_status sv_grad_norm(const void *const *tensors, const int64_t *sizes, const int *dtypes, int64_t count, float *norm,
+                       void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * The same norm N (before its rounding), and every value scaled by
+ *   k = min(1, max_norm / (N + 1e-6))        rounded to float32 (subnormal
+ *                                            below 2^-126)
+ * out = g * k, a float32 product rounded to the tensor's type.  With N = Inf k
+ * is 0 (an Inf itself becomes NaN); with N = NaN every value becomes NaN.
+ *   out        host array of device addresses; out[i] may be tensors[i] (in
+ *              place), else what is written must not overlap what is read or
+ *              written for any tensor (SV_ERR_INVALID_ARGUMENT)
+ *   max_norm   >= 0 (Inf: nothing is scaled)
+ * The other arguments and the workspace as for sv_grad_norm.
+ */
+sv_status sv_clip_grad_norm(const void *const *tensors, void *const *out, const int64_t *sizes, const int *dtypes,
+                            int64_t count, double max_norm, float *norm, void *workspace, size_t workspace_bytes,
+                            void *stream);
 
 /*
  * Measurement aid, not part of the method: reads x[0 .. n) once from HBM with

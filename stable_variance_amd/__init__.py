@@ -13,9 +13,16 @@ no GPU is visible, the calls raise.
     layer_norm(x, weight, bias), layer_norm_backward(...)
                                    -> layer norm of rows on the variance's
                                       statistics, and its gradients
+    rms_norm(x, weight, eps, residual), rms_norm_fp8(...), rms_norm_backward(...)
+                                   -> root-mean-square norm of rows with the
+                                      residual's addition, the same in 8 bits
+                                      with scales, and its gradients
     embedding(ids, table, scale), embedding_backward(...)
                                    -> rows of a table, and the table's
                                       gradient as compensated sums by token
+    grad_norm(grads), clip_grad_norm(grads, max_norm, out)
+                                   -> norm of many tensors as one vector, and
+                                      their scaling down to a largest norm
 
 Method: Pennacchio, "Variance in float32 with a first-element shift, a local
 centring and a compensated tree sum", §2 steps 1-4.
@@ -29,7 +36,8 @@ import threading
 from .build import LIB as _LIB_PATH
 
 __all__ = ["tree_sum", "var", "var_variant", "capi", "library_path", "SvError", "set_tuning", "VARIANTS",
-           "layer_norm", "layer_norm_backward", "embedding", "embedding_backward"]
+           "layer_norm", "layer_norm_backward", "rms_norm", "rms_norm_fp8", "rms_norm_backward", "embedding",
+           "embedding_backward", "grad_norm", "clip_grad_norm"]
 
 SV_OK = 0
 _STATUS = {1: "SV_ERR_INVALID_ARGUMENT", 2: "SV_ERR_WORKSPACE", 3: "SV_ERR_NO_DEVICE", 4: "SV_ERR_HIP",
@@ -123,6 +131,24 @@ def capi():
                 L.sv_embedding_backward.restype = cint
                 L.sv_embedding_backward.argtypes = [vp, i64, vp, cint, i64, cint, i64, i64, ctypes.c_float, i64, vp, i64,
                                                     vp, sz, vp]
+                cdouble = ctypes.c_double
+                L.sv_rms_norm.restype = cint
+                L.sv_rms_norm.argtypes = [vp, i64, vp, i64, cint, cint, i64, i64, vp, cint, cdouble, vp, i64, vp, i64,
+                                          vp, vp]
+                L.sv_rms_norm_fp8.restype = cint
+                L.sv_rms_norm_fp8.argtypes = [vp, i64, vp, i64, cint, cint, i64, i64, vp, cint, cdouble, cint, i64, vp,
+                                              i64, vp, vp, i64, vp, vp]
+                L.sv_rms_norm_backward_workspace_size.restype = sz
+                L.sv_rms_norm_backward_workspace_size.argtypes = [i64, i64, cint, cint]
+                L.sv_rms_norm_backward.restype = cint
+                L.sv_rms_norm_backward.argtypes = [vp, i64, vp, i64, vp, i64, cint, cint, i64, i64, vp, cint, vp, vp,
+                                                   i64, vp, i64, vp, vp, sz, vp]
+                L.sv_grad_norm_workspace_size.restype = sz
+                L.sv_grad_norm_workspace_size.argtypes = [vp, vp, i64]
+                L.sv_grad_norm.restype = cint
+                L.sv_grad_norm.argtypes = [vp, vp, vp, i64, vp, vp, sz, vp]
+                L.sv_clip_grad_norm.restype = cint
+                L.sv_clip_grad_norm.argtypes = [vp, vp, vp, vp, i64, cdouble, vp, vp, sz, vp]
                 L.sv_probe_read_bandwidth.restype = ctypes.c_int
                 L.sv_probe_read_bandwidth.argtypes = [vp, i64, vp, vp]
                 _lib = L
@@ -343,9 +369,12 @@ def var_variant(x, variant, dim: int = -1, ddof: int = 0, return_mean: bool = Fa
 
 def __getattr__(name):
     # the autograd functions need torch at import time, the rest only in use
-    if name in ("layer_norm", "layer_norm_backward", "embedding", "embedding_backward"):
-        from . import layers
-
-        globals()[name] = fn = getattr(layers, name)
-        return fn
-    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+    if name in ("layer_norm", "layer_norm_backward", "rms_norm", "rms_norm_fp8", "rms_norm_backward", "embedding",
+                "embedding_backward"):
+        from . import layers as module
+    elif name in ("grad_norm", "clip_grad_norm"):
+        from . import gradients as module
+    else:
+        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+    globals()[name] = fn = getattr(module, name)
+    return fn

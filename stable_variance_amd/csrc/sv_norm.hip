@@ -36,20 +36,6 @@ constexpr int64_t ROW_GRID = 8192;     // workgroups of a row launch, at most
 constexpr int COL_ROWS = 64;           // rows of one partial column sum
 constexpr int64_t COL_MAX_GROUPS = 512;
 
-// 1 / sqrt(v) in double (one Newton step from the hardware's estimate, about
-// 2^-46), so that the float32 value is the rounded one; 0, Inf and NaN as
-// the estimate gives them.  Above float32's range (var = 0 and eps below
-// 8.6e-78) it is the largest finite value: with Inf, equal values would give
-// 0 * Inf = NaN in place of the bias, and NaN gradients.
-__device__ __forceinline__ float rstd_of(float var, double eps) {
-  const double v = (double)var + eps;
-  const double r = __builtin_amdgcn_rsq(v);
-  const double e = 1.0 - v * r * r;
-  const double s = r + 0.5 * r * e;
-  const float f = (float)(__builtin_isfinite(e) ? s : r);
-  return v > 0.0 && f > __FLT_MAX__ ? __FLT_MAX__ : f;
-}
-
 // Sum of one node per thread over the workgroup, in a fixed order; every
 // thread gets the root's value.  `lds` holds a node per wave.
 template <int WAVES>
@@ -134,7 +120,7 @@ __global__ __launch_bounds__(tpb(L)) void k_norm_rows(
     svr::group_sum<L, 2>(s, lds_b);
     const float b = s[0] * inv_n;
     const float q = s[1] * inv_n - b * b;
-    const float rs = rstd_of(q <= 0.0f ? 0.0f : q, eps);  // a NaN stays
+    const float rs = svr::rstd_of((double)(q <= 0.0f ? 0.0f : q) + eps);  // a NaN stays
     if (R == 1 || r < rows) {
       if (l == 0) {
         if (mean) mean[r] = m1 + b;
@@ -249,7 +235,7 @@ __global__ __launch_bounds__(ROW_THREADS) void k_norm_any(const T *__restrict__ 
     const float b = block_sum<ROW_THREADS / 64>(s1, lds) / fn;
     const float q = block_sum<ROW_THREADS / 64>(s2, lds) / fn - b * b;
     const float var = q <= 0.0f ? 0.0f : q;  // a NaN stays
-    const float rs = rstd_of(var, eps);
+    const float rs = svr::rstd_of((double)var + eps);
     if (threadIdx.x == 0) {
       if (mean) mean[r] = m1 + b;
       if (rstd) rstd[r] = rs;

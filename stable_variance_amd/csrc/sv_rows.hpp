@@ -100,10 +100,23 @@ __device__ __forceinline__ void put_chunk(T *__restrict__ p, int e, int count, c
   }
 }
 
+// 1 / sqrt(v) in double (one Newton step from the hardware's estimate, about
+// 2^-46), so that the float32 value is the rounded one; 0, Inf and NaN as
+// the estimate gives them.  Above float32's range (a variance or mean square
+// of 0 and eps below 8.6e-78) it is the largest finite value: with Inf, zeros
+// would give 0 * Inf = NaN in place of 0, and NaN gradients.
+__device__ __forceinline__ float rstd_of(double v) {
+  const double r = __builtin_amdgcn_rsq(v);
+  const double e = 1.0 - v * r * r;
+  const double s = r + 0.5 * r * e;
+  const float f = (float)(__builtin_isfinite(e) ? s : r);
+  return v > 0.0 && f > __FLT_MAX__ ? __FLT_MAX__ : f;
+}
+
 // Pairwise sum of N values fn(OFF), fn(OFF + 1), .. (adjacent pairs at each
-// level).
+// level), of fn's type.
 template <int OFF, int N, class Fn>
-__device__ __forceinline__ float pair_sum(Fn &&fn) {
+__device__ __forceinline__ auto pair_sum(Fn &&fn) {
   if constexpr (N == 1) return fn(OFF);
   else return pair_sum<OFF, (N + 1) / 2>(fn) + pair_sum<OFF + (N + 1) / 2, N / 2>(fn);
 }

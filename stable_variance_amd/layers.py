@@ -1,13 +1,15 @@
-"""Layer norm and embedding: forward and backward calls of the C ABI.
+"""Layer norm, root-mean-square norm and embedding: forward and backward calls
+of the C ABI.
 
 Like the rest of the binding these functions only marshal arguments.  Tensors
 are float32, bfloat16 or float16 on one HIP device; every call runs on the
 current stream of that device, allocates its outputs and scratch from torch's
 allocator (so it can be captured in a HIP graph) and does not synchronise.
-``layer_norm`` and ``embedding`` take part in autograd: their gradients are
-``layer_norm_backward`` and ``embedding_backward``, which are plain calls
-without a derivative of their own.  There is no forward-mode derivative: a
-dual tensor is refused (``NotImplementedError``).
+``layer_norm``, ``rms_norm`` and ``embedding`` take part in autograd: their
+gradients are ``layer_norm_backward``, ``rms_norm_backward`` and
+``embedding_backward``, which are plain calls without a derivative of their
+own.  There is no forward-mode derivative: a dual tensor is refused
+(``NotImplementedError``).
 
 A captured backward pass is subject to torch's own rule: no eager graph of
 the same leaves may be alive while it is captured, as their gradients would
@@ -25,7 +27,8 @@ from torch.autograd import forward_ad
 
 from . import SvError, _check, capi
 
-__all__ = ["layer_norm", "layer_norm_backward", "embedding", "embedding_backward"]
+__all__ = ["layer_norm", "layer_norm_backward", "rms_norm", "rms_norm_fp8", "rms_norm_backward", "embedding",
+           "embedding_backward"]
 
 _CODES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 _TYPES = tuple(_CODES)
@@ -50,7 +53,7 @@ def _no_tangents(*tensors):
     result without its tangent would pass for a constant."""
     if forward_ad._current_level >= 0 and any(
             isinstance(t, torch.Tensor) and forward_ad.unpack_dual(t).tangent is not None for t in tensors):
-        raise NotImplementedError("the layer norm and the embedding have no forward-mode derivative")
+        raise NotImplementedError("the norms and the embedding have no forward-mode derivative")
 
 
 def _same_device(ref, t, name):
@@ -225,6 +228,190 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, *, weight_grad: bool = T
     elif param_dtype not in (x.dtype, torch.float32):
         raise TypeError(f"param_dtype must be {x.dtype} or torch.float32, got {param_dtype}")
     return _norm_backward(dy, x, mean, rstd, weight, True, bool(weight_grad), bool(bias_grad), param_dtype)
+
+
+# ---------------------------------------------------------------- root-mean-square norm
+
+_FP8 = {torch.float8_e4m3fn: 3, torch.float8_e5m2: 4}
+_BLOCK = 128  # values that share a scale
+
+
+def _rms_inputs(x, weight, residual, rows, n):
+    """Checked and stored: x, its row stride, the residual, its row stride and
+    type code, the weight and its type."""
+    w = _param(weight, "weight", x, n) if weight is not None else None
+    x2, ldx = _rows(x, rows, n)
+    if residual is None:
+        return x2, ldx, None, n, _CODES[x.dtype], w
+    _tensor(residual, "residual", (x.dtype, torch.float32) if x.dtype != torch.float32 else (torch.float32,))
+    _same_device(x, residual, "residual")
+    if residual.shape != x.shape:
+        raise ValueError(f"residual has shape {tuple(residual.shape)}, x {tuple(x.shape)}")
+    r2, ldr = _rows(residual, rows, n)
+    return x2, ldx, r2, ldr, _CODES[residual.dtype], w
+
+
+def _rms_forward(x, weight, eps, residual, want_rstd):
+    rows, n = _shape_2d(x, "x")
+    x2, ldx, r2, ldr, sum_code, w = _rms_inputs(x, weight, residual, rows, n)
+    code = _CODES[x.dtype]
+    with _on(x.device):
+        y = torch.empty_like(x, memory_format=torch.contiguous_format)
+        h = None if residual is None else torch.empty_like(residual, memory_format=torch.contiguous_format)
+        rstd = x.new_empty(x.shape[:-1], dtype=torch.float32) if want_rstd else None
+        _check(capi().sv_rms_norm(_ptr(x2), ldx, _ptr(r2), ldr, code, sum_code, rows, n, _ptr(w),
+                                  code if w is None else _CODES[w.dtype], eps, _ptr(y), n, _ptr(h), n, _ptr(rstd),
+                                  _raw_stream(x.device.index)))
+    return y, h, rstd
+
+
+class _RmsNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, residual, eps):
+        y, h, rstd = _rms_forward(x, weight, eps, residual, True)
+        ctx.save_for_backward(x if h is None else h, weight, rstd)
+        ctx.x_dtype = x.dtype
+        ctx.mark_non_differentiable(rstd)
+        ctx.set_materialize_grads(False)
+        return y, h, rstd
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy, dsum, _rstd):
+        h, weight, rstd = ctx.saved_tensors
+        need_x, need_w, need_r, _ = ctx.needs_input_grad
+        mixed = h.dtype != ctx.x_dtype
+        if dy is None:  # y took no part
+            dx = dsum.to(ctx.x_dtype) if need_x and dsum is not None else None
+            return dx, None, dsum if need_r else None, None
+        dh, dx, dw = _rms_backward(dy, h, rstd, weight, dsum, need_r or (need_x and not mixed), need_x and mixed, need_w,
+                                   weight.dtype if weight is not None else None)
+        return dx if mixed else dh if need_x else None, dw, dh if need_r else None, None
+
+
+def rms_norm(x, weight=None, eps: float = 1e-6, residual=None, return_rstd: bool = False):
+    """Root-mean-square norm over the last dimension: ``x / sqrt(mean(x^2) +
+    eps) * weight``, the squares summed in float64, the rest computed in
+    float32 and rounded once to x's type.
+
+    With a ``residual`` (x's shape; x's type or float32) the norm is of ``h =
+    x + residual``, rounded to the residual's type, and ``(y, h)`` is returned.
+    ``weight`` (optional) has shape ``[n]`` and x's type or float32.  With
+    ``return_rstd`` also ``1 / sqrt(mean(h^2) + eps)`` of each row (float32,
+    not differentiable), which ``rms_norm_backward`` takes.  Rows may be
+    strided; a last dimension that is not contiguous is copied first.  A row's
+    result does not depend on the other rows.
+    """
+    _tensor(x, "x", _TYPES)
+    _no_tangents(x, weight, residual)
+    eps = float(eps)
+    # what is no tensor is refused where the other arguments are checked
+    if torch.is_grad_enabled() and (x.requires_grad or getattr(weight, "requires_grad", False)
+                                    or getattr(residual, "requires_grad", False)):
+        y, h, rstd = _RmsNorm.apply(x, weight, residual, eps)
+    else:
+        y, h, rstd = _rms_forward(x, weight, eps, residual, return_rstd)
+    if residual is None:
+        return (y, rstd) if return_rstd else y
+    return (y, h, rstd) if return_rstd else (y, h)
+
+
+def rms_norm_fp8(x, weight=None, eps: float = 1e-6, residual=None, dtype=torch.float8_e4m3fn, block=128,
+                 return_rstd: bool = False):
+    """``rms_norm`` with its output in 8 bits: ``(q, scale)``, with a residual
+    ``(q, scale, h)``, and ``rstd`` behind these with ``return_rstd``.
+
+    ``dtype`` is ``torch.float8_e4m3fn`` or ``torch.float8_e5m2``.  ``scale``
+    (float32) is the largest magnitude of a block of 128 values of a row over
+    the type's largest value: shape ``x.shape[:-1] + (ceil(n / 128),)``, or
+    with ``block=None`` one for the whole row, ``x.shape[:-1] + (1,)``.  ``q *
+    scale`` stands for the norm, which is rounded once, from float32.  There is
+    no gradient: inputs that require one are refused while gradients are
+    enabled.  A training step calls it under ``torch.no_grad()`` and
+    ``rms_norm_backward`` with the ``h`` (or x) and ``rstd`` it left.
+    """
+    _tensor(x, "x", _TYPES)
+    _no_tangents(x, weight, residual)
+    if torch.is_grad_enabled() and any(getattr(t, "requires_grad", False) for t in (x, weight, residual)):
+        raise NotImplementedError("rms_norm_fp8 has no gradient: call it under torch.no_grad()")
+    if dtype not in _FP8:
+        raise TypeError(f"dtype must be {' or '.join(str(d) for d in _FP8)}, got {dtype}")
+    if block is not None and (isinstance(block, bool) or operator.index(block) != _BLOCK):
+        raise ValueError(f"block must be {_BLOCK}, or None for whole rows, got {block}")
+    rows, n = _shape_2d(x, "x")
+    x2, ldx, r2, ldr, sum_code, w = _rms_inputs(x, weight, residual, rows, n)
+    code = _CODES[x.dtype]
+    with _on(x.device):
+        q = torch.empty_like(x, dtype=dtype, memory_format=torch.contiguous_format)
+        scale = x.new_empty(x.shape[:-1] + (1 if block is None else -(-n // _BLOCK),), dtype=torch.float32)
+        h = None if residual is None else torch.empty_like(residual, memory_format=torch.contiguous_format)
+        rstd = x.new_empty(x.shape[:-1], dtype=torch.float32) if return_rstd else None
+        _check(capi().sv_rms_norm_fp8(_ptr(x2), ldx, _ptr(r2), ldr, code, sum_code, rows, n, _ptr(w),
+                                      code if w is None else _CODES[w.dtype], float(eps), _FP8[dtype],
+                                      0 if block is None else _BLOCK, _ptr(q), n, _ptr(scale), _ptr(h), n, _ptr(rstd),
+                                      _raw_stream(x.device.index)))
+    return (q, scale) + (() if h is None else (h,)) + (() if rstd is None else (rstd,))
+
+
+def _rms_backward(dy, h, rstd, weight, dsum, need_dh, need_dx, need_w, param_dtype):
+    _no_tangents(dy, h, rstd, weight, dsum)
+    rows, n = _shape_2d(h, "h")
+    w = _param(weight, "weight", dy, n) if weight is not None else None
+    dy2, lddy = _rows(dy, rows, n)
+    h2, ldh = _rows(h, rows, n)
+    d2, ldd = _rows(dsum, rows, n) if dsum is not None else (None, n)
+    rstd = _stored(rstd)
+    code, sum_code = _CODES[dy.dtype], _CODES[h.dtype]
+    L = capi()
+    with _on(h.device):
+        dh = torch.empty_like(h, memory_format=torch.contiguous_format) if need_dh else None
+        dx = torch.empty_like(dy, memory_format=torch.contiguous_format) if need_dx else None
+        dw = torch.empty(n, dtype=param_dtype, device=h.device) if need_w else None
+        nbytes = L.sv_rms_norm_backward_workspace_size(rows, n, code, sum_code) if need_w else 0
+        ws = _scratch(nbytes, h.device, "rms_norm_backward")
+        _check(L.sv_rms_norm_backward(_ptr(dy2), lddy, _ptr(h2), ldh, _ptr(d2), ldd, code, sum_code, rows, n, _ptr(w),
+                                      code if param_dtype is None else _CODES[param_dtype], _ptr(rstd), _ptr(dh), n,
+                                      _ptr(dx), n, _ptr(dw), _ptr(ws), nbytes, _raw_stream(h.device.index)))
+    return dh, dx, dw
+
+
+def rms_norm_backward(dy, h, rstd, weight=None, dsum=None, *, weight_grad: bool = True, param_dtype=None):
+    """Gradients ``(dh, dweight)`` of ``rms_norm`` at the rows ``h`` that were
+    normed (x, or the sum it returned), for the gradient ``dy`` of its result
+    and, with a residual, the gradient ``dsum`` of the sum, from the ``rstd``
+    it returned.
+
+    ``dh``, in h's type, is the gradient of x and of the residual alike.
+    ``dweight`` has the weight's type (``param_dtype``, dy's type or float32,
+    when there is no weight; float32 by default) and is None where not asked
+    for.
+    """
+    _tensor(dy, "dy", _TYPES)
+    _tensor(h, "h", (dy.dtype, torch.float32) if dy.dtype != torch.float32 else (torch.float32,))
+    _same_device(h, dy, "dy")
+    if dy.shape != h.shape:
+        raise ValueError(f"dy has shape {tuple(dy.shape)}, h {tuple(h.shape)}")
+    _shape_2d(h, "h")
+    _tensor(rstd, "rstd", (torch.float32,))
+    _same_device(h, rstd, "rstd")
+    if rstd.shape != h.shape[:-1]:
+        raise ValueError(f"rstd must have shape {tuple(h.shape[:-1])}, got {tuple(rstd.shape)}")
+    if dsum is not None:
+        _tensor(dsum, "dsum", (h.dtype,))
+        _same_device(h, dsum, "dsum")
+        if dsum.shape != h.shape:
+            raise ValueError(f"dsum has shape {tuple(dsum.shape)}, h {tuple(h.shape)}")
+    if weight is not None:
+        _tensor(weight, "weight", (dy.dtype, torch.float32))
+        if param_dtype not in (None, weight.dtype):
+            raise TypeError(f"param_dtype {param_dtype} differs from the weight's {weight.dtype}")
+        param_dtype = weight.dtype
+    elif param_dtype is None:
+        param_dtype = torch.float32
+    elif param_dtype not in (dy.dtype, torch.float32):
+        raise TypeError(f"param_dtype must be {dy.dtype} or torch.float32, got {param_dtype}")
+    dh, _, dw = _rms_backward(dy, h, rstd, weight, dsum, True, False, bool(weight_grad), param_dtype)
+    return dh, dw
 
 
 # ---------------------------------------------------------------- embedding
