@@ -211,7 +211,34 @@ __device__ __forceinline__ void put_fp8(uint8_t *p, int count, const float (&f)[
   }
 }
 
-// ---------------------------------------------------------------- host
+// ---------------------------------------------------------------- calls
+
+constexpr int ROW_THREADS = 512;
+constexpr int64_t ROW_GRID = 8192;  // workgroups of a row launch, at most
+constexpr int BLOCK = 128;          // values that share a scale
+
+// Values of one chunk of threads that hold T and S side by side: 16 bytes of
+// the wider type.
+template <class T, class S>
+constexpr int chunk_values() { return 16 / (int)(sizeof(T) > sizeof(S) ? sizeof(T) : sizeof(S)); }
+
+// What a call passes on about its rows.
+struct Rows {
+  int64_t rows;
+  int n;
+  const void *w;
+  int pt;
+  double eps;
+  float *rstd;
+};
+
+// The 8-bit output.
+struct Out8 {
+  uint8_t *q;
+  int64_t ldq;
+  float *scale;  // one for each block of 128 values, or (per_row) for each row
+  bool per_row, e5m2;
+};
 
 // Calls fn(T{}, S{}) with the element types of x and of the residual stream
 // (T, or float32).
@@ -223,5 +250,45 @@ inline void with_types(int dtype, int sum_dtype, Fn &&fn) {
     else fn(t, float{});
   });
 }
+
+// Checks that the calls share; SV_OK without touching the message.
+inline sv_status check_rows(const char *who, int dtype, int sum_dtype, int64_t rows, int64_t n, int param_dtype) {
+  if (!svr::dtype_bytes(dtype)) return svh::fail(SV_ERR_INVALID_ARGUMENT, "%s: dtype %d is not a type code", who, dtype);
+  if (sum_dtype != dtype && sum_dtype != SV_DTYPE_F32)
+    return svh::fail(SV_ERR_INVALID_ARGUMENT, "%s: sum_dtype %d must be dtype or SV_DTYPE_F32", who, sum_dtype);
+  if (param_dtype != dtype && param_dtype != SV_DTYPE_F32)
+    return svh::fail(SV_ERR_INVALID_ARGUMENT, "%s: param_dtype %d must be the rows' type or SV_DTYPE_F32", who,
+                param_dtype);
+  if (rows < 0 || n < 0)
+    return svh::fail(SV_ERR_INVALID_ARGUMENT, "%s: rows = %lld, n = %lld must be >= 0", who, (long long)rows,
+                (long long)n);
+  if (n > svr::MAX_N) return svh::fail(SV_ERR_UNSUPPORTED, "%s: rows of %lld values exceed 2^27", who, (long long)n);
+  if (n > 0 && rows > svr::MAX_VALUES / n)
+    return svh::fail(SV_ERR_UNSUPPORTED, "%s: %lld x %lld values exceed 2^36", who, (long long)rows, (long long)n);
+  if (rows > svr::MAX_VALUES) return svh::fail(SV_ERR_UNSUPPORTED, "%s: %lld rows exceed 2^36", who, (long long)rows);
+  return SV_OK;
+}
+
+// Checks of the forward calls.
+inline sv_status check_forward(const char *who, const void *x, int64_t ldx, const void *residual, int64_t ldr, int dtype,
+                        int sum_dtype, int64_t rows, int64_t n, const void *weight, int param_dtype, double eps,
+                        const void *sum, int64_t ldsum) {
+  sv_status st = check_rows(who, dtype, sum_dtype, rows, n, param_dtype);
+  if (st != SV_OK) return st;
+  if (!(eps >= 0.0) || eps > 3.0e38) return svh::fail(SV_ERR_INVALID_ARGUMENT, "%s: eps must be >= 0 and finite", who);
+  const size_t e = svr::dtype_bytes(dtype), se = svr::dtype_bytes(sum_dtype);
+  if ((st = svr::check_matrix(who, "x", x, ldx, rows, n, e)) != SV_OK) return st;
+  if (residual || sum) {
+    if ((st = svr::check_matrix(who, "residual", residual, ldr, rows, n, se)) != SV_OK) return st;
+    if ((st = svr::check_matrix(who, "sum", sum, ldsum, rows, n, se)) != SV_OK) return st;
+  } else if (sum_dtype != dtype) {
+    return svh::fail(SV_ERR_INVALID_ARGUMENT, "%s: sum_dtype %d without a residual must be dtype", who, sum_dtype);
+  }
+  if (weight && (st = svr::check_matrix(who, "weight", weight, n, 1, n, svr::dtype_bytes(param_dtype))) != SV_OK)
+    return st;
+  return SV_OK;
+}
+
+inline unsigned row_grid(int64_t rows) { return (unsigned)(rows < ROW_GRID ? rows : ROW_GRID); }
 
 }  // namespace svm

@@ -53,12 +53,12 @@ struct Chunk {
 };
 
 template <bool NT, class T, class Vec>
-__device__ __forceinline__ void store16(T *p, Vec v) {
+__device__ __forceinline__ void store_chunk_at(T *p, Vec v) {
   if constexpr (NT) {
     typedef Vec Unaligned __attribute__((aligned(sizeof(T))));
     __builtin_nontemporal_store(v, reinterpret_cast<Unaligned *>(p));
   } else {
-    __builtin_memcpy(p, &v, 16);
+    __builtin_memcpy(p, &v, sizeof(Vec));
   }
 }
 
@@ -122,17 +122,18 @@ __device__ __forceinline__ auto pair_sum(Fn &&fn) {
 }
 
 // A row of n values held by L threads, K chunks each: thread l's chunk k
-// starts at value (k * L + l) * VE.  FIT says what is known of n:
+// starts at value (k * L + l) * VE.  A chunk is 16 bytes, or has the number of
+// values of a wider type that is held beside T.  FIT says what is known of n:
 //   FIT_FULL    n == K * L * VE: every chunk is whole
 //   FIT_CHUNKS  n is a multiple of VE: a chunk is whole or outside
 //   FIT_ANY     the row's last chunk may be part of one
 //   FIT_SMALL   n < VE: one thread holds the row and loads value by value
 enum Fit { FIT_FULL = 0, FIT_CHUNKS = 1, FIT_ANY = 2, FIT_SMALL = 3 };
 
-template <class T, int L, int K, int FIT>
+template <class T, int L, int K, int FIT, int VALUES = Chunk<T>::VE>
 struct RowTile {
-  static constexpr int VE = Chunk<T>::VE, E = K * VE;
-  using Vec = typename Chunk<T>::Vec;
+  static constexpr int VE = VALUES, E = K * VE;
+  typedef T Vec __attribute__((ext_vector_type(VALUES)));
 
   __device__ static __forceinline__ int first(int l, int k) { return (k * L + l) * VE; }
   // Chunk k holds values of the row.
@@ -162,21 +163,24 @@ struct RowTile {
         const bool ok = FIT == FIT_ANY ? e < n && e + VE <= avail : e < n;
         e = ok ? e : 0;  // avail >= n >= VE
       }
-      __builtin_memcpy(&raw[k], p + e, 16);
+      __builtin_memcpy(&raw[k], p + e, sizeof(Vec));
     }
   }
 
   // Waits for the loads here, so that the stores that follow are not waited
   // for as well where the values are first used.
-  template <class S>
-  __device__ static __forceinline__ void arrived(Vec (&raw)[K], S &one) {
-    typedef unsigned U4 __attribute__((ext_vector_type(4)));
+  __device__ static __forceinline__ void arrived(Vec (&raw)[K]) {
+    typedef unsigned Bits __attribute__((ext_vector_type(sizeof(Vec) / 4)));
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      U4 u = __builtin_bit_cast(U4, raw[k]);
+      Bits u = __builtin_bit_cast(Bits, raw[k]);
       asm volatile("" : "+v"(u));
       raw[k] = __builtin_bit_cast(Vec, u);
     }
+  }
+  template <class S>
+  __device__ static __forceinline__ void arrived(Vec (&raw)[K], S &one) {
+    arrived(raw);
     using Bits = std::conditional_t<sizeof(S) == 2, unsigned short, unsigned>;
     unsigned b = __builtin_bit_cast(Bits, one);
     asm volatile("" : "+v"(b));
@@ -242,7 +246,7 @@ struct RowTile {
 #pragma unroll
     for (int i = 0; i < VE; ++i) v[i] = from_f<T>(f[k * VE + i]);
     if (FIT == FIT_FULL || FIT == FIT_CHUNKS || e + VE <= n) {
-      store16<NT>(p + e, v);
+      store_chunk_at<NT>(p + e, v);
     } else {
       // 4, 2 and 1 of the values that are left, as their number's bits say
       const int left = n - e;
