@@ -15,6 +15,188 @@ namespace {
 constexpr int COL_ROWS = 64;  // rows of one partial column sum
 constexpr int64_t COL_MAX_GROUPS = 512;
 
+// ---------------------------------------------------------------- rows in registers
+
+// Threads of a workgroup of the backward pass: one workgroup per CU with as
+// many waves as the registers of E values allow, since every workgroup leaves
+// one partial column sum.
+constexpr int grad_tpb(int L, int E, int VE) {
+  return (E <= 8 || L > 512 ? 1024 : E <= 16 && VE == 8 && L <= 256 ? 768 : 512) / L * L;
+}
+constexpr int64_t GRAD_BLOCKS = 256;  // one workgroup per CU
+// Rows that one thread adds up in plain float32 for the columns' sums; the
+// workgroup's groups and then the workgroups are joined with compensation.
+constexpr int64_t GRAD_RUN = 32;
+
+// The backward pass of rows that a group of L threads holds in registers, K
+// chunks per thread: dy, h and (SUM) dsum are read once, one cross-thread sum
+// per row gives c.  The column sums of the rows a group passes stay in
+// registers; at the end the workgroup's groups are added up through LDS into
+// its row of `part`, [gridDim.x][n] (part == nullptr: not asked for).  What is
+// written is stored non-temporal.
+template <class T, class S, bool SUM, int L, int K, int FIT>
+__global__ __launch_bounds__(grad_tpb(L, K * svm::chunk_values<T, S>(), svm::chunk_values<T, S>())) void k_rms_grad(
+    const T *__restrict__ dy, int64_t lddy, const S *__restrict__ h, int64_t ldh, const S *__restrict__ dsum,
+    int64_t ldds, Rows a, S *__restrict__ dh, int64_t lddh, T *__restrict__ dx, int64_t lddx,
+    float *__restrict__ part) {
+  constexpr int VE = svm::chunk_values<T, S>(), E = K * VE, TPB = grad_tpb(L, E, VE), R = TPB / L;
+  using TT = svr::RowTile<T, L, K, FIT, VE>;
+  using TS = svr::RowTile<S, L, K, FIT, VE>;
+  // 1024 threads leave 128 registers each: the weight then waits in LDS (a
+  // thread reads back what it wrote) and the next row is loaded after this one
+  constexpr bool FEW = L > 512;
+  __shared__ float wlds[FEW ? TPB * E : 1];
+  __shared__ float lds[2][TPB / 64];
+  __shared__ float cols[TPB * E];
+  const int64_t rows = a.rows;
+  const int n = a.n, g = svr::group_of<L>(), l0 = threadIdx.x % L;
+  const float inv_n = 1.0f / (float)n;
+  float wv[FEW ? 1 : K][VE], aw[E];
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    const int e = TT::first(l0, k), left = n - e;
+    svm::get_weight<VE>(a.w, a.pt, e, left < 0 ? 0 : left, wv[FEW ? 0 : k]);
+    if constexpr (FEW) {
+#pragma unroll
+      for (int i = 0; i < VE; ++i) wlds[e + i] = wv[0][i];
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < E; ++i) aw[i] = 0.0f;
+  const int64_t step = (int64_t)gridDim.x * R;
+  typename TS::Vec rh[K], rd[SUM ? K : 1];
+  typename TT::Vec rg[K];
+  int64_t r = (int64_t)blockIdx.x * R + g;
+  int64_t rl = R == 1 || r < rows ? r : rows - 1;  // the row that is loaded
+  float rs_next;
+  const auto load = [&](int l) {
+    TS::load(h + rl * ldh, n, TS::avail(rows, rl, ldh, n), l, rh);
+    TT::load(dy + rl * lddy, n, TT::avail(rows, rl, lddy, n), l, rg);
+    if constexpr (SUM) TS::load(dsum + rl * ldds, n, TS::avail(rows, rl, ldds, n), l, rd);
+    rs_next = a.rstd[rl];
+  };
+  const auto arrived = [&] {
+    TS::arrived(rh, rs_next);
+    TT::arrived(rg);
+    if constexpr (SUM) TS::arrived(rd);
+  };
+  load(l0);
+  if constexpr (!FEW) arrived();
+  int turn = 0;
+  for (int64_t r0 = (int64_t)blockIdx.x * R; r0 < rows; r0 += step, r += step, turn ^= 1) {
+    int l = l0;  // opaque, so that the addresses of all chunks are not kept in registers across rows
+    asm volatile("" : "+v"(l));
+    float x[E], v[E], d[SUM ? E : 1];
+    TS::unpack(rh, x);
+    TT::unpack(rg, v);
+    TS::load_rest(h + rl * ldh, n, TS::avail(rows, rl, ldh, n), l, x);
+    TT::load_rest(dy + rl * lddy, n, TT::avail(rows, rl, lddy, n), l, v);
+    if constexpr (SUM) {
+      TS::unpack(rd, d);
+      TS::load_rest(dsum + rl * ldds, n, TS::avail(rows, rl, ldds, n), l, d);
+    }
+    const float rs = rs_next;
+    rl = r + step < rows ? r + step : rows - 1;
+    if constexpr (!FEW) load(l);
+    TS::set_rest(n, l, 0.0f, x);
+    TT::set_rest(n, l, 0.0f, v);
+    const auto weight = [&](int i) { return FEW ? wlds[TT::first(l, i / VE) + i % VE] : wv[FEW ? 0 : i / VE][i % VE]; };
+    const bool own = R == 1 || r < rows;
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      x[i] = x[i] * rs;
+      if (own) aw[i] = aw[i] + v[i] * x[i];
+      v[i] = v[i] * weight(i);
+    }
+    float s[1] = {TT::sum(n, l, [&](int i) { return v[i] * x[i]; })};
+    svr::group_sum<L, 1>(s, lds[turn]);
+    const float c = s[0] * inv_n;
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      v[i] = rs * (v[i] - x[i] * c);
+      if constexpr (SUM) v[i] = v[i] + d[i];
+    }
+    if constexpr (!FEW) arrived();
+    if (own && dh) {
+#pragma unroll
+      for (int k = 0; k < K; ++k) TS::template store_chunk<true>(dh + r * lddh, n, l, k, v);
+    }
+    if (own && dx) {
+#pragma unroll
+      for (int k = 0; k < K; ++k) TT::template store_chunk<true>(dx + r * lddx, n, l, k, v);
+    }
+    if constexpr (FEW) {
+      __builtin_amdgcn_sched_barrier(0);
+      load(l);
+    }
+  }
+  if (!part) return;
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < K; ++k)
+#pragma unroll
+    for (int i = 0; i < VE; ++i) cols[g * (L * E) + TT::first(l0, k) + i] = aw[k * VE + i];
+  __syncthreads();
+  float *out = part + (int64_t)blockIdx.x * n;
+  for (int j = threadIdx.x; j < n; j += TPB) {
+    Node t = sv::zero_node();
+    for (int q = 0; q < R; ++q) svr::add_to(t, cols[q * (L * E) + j]);
+    out[j] = sv::root_value(t);
+  }
+}
+
+// Calls fn(L, K, FIT) (integral constants) with the smallest tile of VE-value
+// chunks that holds n values; false when none does.
+template <int VE, class Fn>
+bool with_tile(int64_t n, Fn &&fn) {
+  if (n < 1) return false;
+  const auto tile = [&](auto tl, auto tk) {
+    constexpr int L = decltype(tl)::value, K = decltype(tk)::value;
+    if constexpr (L == 1) {
+      if (n < VE) {
+        fn(tl, tk, std::integral_constant<int, svr::FIT_SMALL>{});
+        return true;
+      }
+    }
+    if (n > (int64_t)L * K * VE) return false;
+    constexpr bool WHOLE = L > 512;  // whole chunks only: no register is left for the others
+    if (n % VE == 0) {
+      fn(tl, tk, std::integral_constant<int, svr::FIT_CHUNKS>{});
+      return true;
+    }
+    if constexpr (!WHOLE) fn(tl, tk, std::integral_constant<int, svr::FIT_ANY>{});
+    return !WHOLE;
+  };
+#define SV_TILE(L, V) \
+  if (tile(std::integral_constant<int, L>{}, std::integral_constant<int, (V) / VE>{})) return true;
+  SV_TILE(1, 8) SV_TILE(2, 8) SV_TILE(4, 8) SV_TILE(8, 8) SV_TILE(8, 16)
+  SV_TILE(16, 16) SV_TILE(32, 16) SV_TILE(64, 16) SV_TILE(64, 24)
+  SV_TILE(128, 16) SV_TILE(256, 16) SV_TILE(256, 24) SV_TILE(512, 16) SV_TILE(512, 24)
+  SV_TILE(1024, 16)
+#undef SV_TILE
+  return false;
+}
+
+// Workgroups of k_rms_grad (0: the rows are too long for it).  Every group of
+// a workgroup passes at most GRAD_RUN rows.
+int64_t grad_blocks(int dtype, int sum_dtype, int64_t rows, int64_t n) {
+  int64_t blocks = 0;
+  svm::with_types(dtype, sum_dtype, [&](auto t, auto u) {
+    constexpr int VE = svm::chunk_values<decltype(t), decltype(u)>();
+    with_tile<VE>(n, [&](auto tl, auto tk, auto) {
+      constexpr int L = decltype(tl)::value, E = decltype(tk)::value * VE;
+      constexpr int64_t R = grad_tpb(L, E, VE) / L;
+      const int64_t all = (rows + R - 1) / R;
+      const int64_t rounds = (all + GRAD_RUN * GRAD_BLOCKS - 1) / (GRAD_RUN * GRAD_BLOCKS);
+      blocks = all < GRAD_BLOCKS ? all : rounds * GRAD_BLOCKS;  // whole rounds of the chip
+      if (blocks < 1) blocks = 1;
+    });
+  });
+  return blocks;
+}
+
+// ---------------------------------------------------------------- longer rows
+
 // The rows' part of the backward pass for rows of any length.
 template <class T, class S>
 __global__ __launch_bounds__(ROW_THREADS) void k_rms_dh_any(const T *dy, int64_t lddy, const S *h, int64_t ldh,
@@ -107,8 +289,12 @@ __global__ __launch_bounds__(64 * COL_WAVES) void k_rms_dw_any(const T *dy, int6
 // Joins the partial sums part[groups][n] of 64 columns: wave i adds up groups
 // i, i + 16, .. in order, then the waves are joined pairwise.  The launch
 // starts at block b0.
+__device__ __forceinline__ Node node_of(float v) { return {v, 0.0f}; }
+__device__ __forceinline__ Node node_of(Node v) { return v; }
+
 constexpr int JOIN_WAVES = 16;
-__global__ __launch_bounds__(64 * JOIN_WAVES) void k_rms_join(const Node *part, int groups, int n, int b0, void *dw,
+template <class P>
+__global__ __launch_bounds__(64 * JOIN_WAVES) void k_rms_join(const P *part, int groups, int n, int b0, void *dw,
                                                               int pt) {
   __shared__ Node lds[JOIN_WAVES][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -116,7 +302,7 @@ __global__ __launch_bounds__(64 * JOIN_WAVES) void k_rms_join(const Node *part, 
   Node s = sv::zero_node();
   if (j < n) {
 #pragma unroll 8
-    for (int q = wave; q < groups; q += JOIN_WAVES) s = sv::combine(s, part[(int64_t)q * n + j]);
+    for (int q = wave; q < groups; q += JOIN_WAVES) s = sv::combine(s, node_of(part[(int64_t)q * n + j]));
   }
   lds[wave][lane] = s;
   __syncthreads();
@@ -126,6 +312,14 @@ __global__ __launch_bounds__(64 * JOIN_WAVES) void k_rms_join(const Node *part, 
     for (int i = 0; i < JOIN_WAVES; ++i) t[i] = lds[i][lane];
     svr::store_as(dw, j, pt, sv::root_value(sv::node_tree<0, JOIN_WAVES, JOIN_WAVES>(t)));
   }
+}
+
+// k_rms_join over all columns, in launches within HIP's limit.
+template <class P>
+void join_columns(const P *part, int64_t groups, int64_t n, void *dw, int pt, hipStream_t s) {
+  svh::in_batches((n + 63) / 64, 1, 64 * JOIN_WAVES, [&](int64_t b0, int64_t blocks) {
+    k_rms_join<P><<<(unsigned)blocks, 64 * JOIN_WAVES, 0, s>>>(part, (int)groups, (int)n, (int)b0, dw, pt);
+  });
 }
 
 // Workgroups of k_rms_dw_any across a row.
@@ -153,6 +347,8 @@ size_t sv_rms_norm_backward_workspace_size(int64_t rows, int64_t n, int dtype, i
       n > svr::MAX_N || rows > svr::MAX_VALUES || (n > 0 && rows > svr::MAX_VALUES / n))
     return (size_t)-1;
   if (n == 0) return 0;
+  const int64_t blocks = grad_blocks(dtype, sum_dtype, rows, n);
+  if (blocks) return svr::round256((size_t)blocks * (size_t)n * sizeof(float));
   return svr::round256((size_t)col_groups(dtype, sum_dtype, rows, n) * (size_t)n * sizeof(Node));
 }
 
@@ -184,22 +380,39 @@ sv_status sv_rms_norm_backward(const void *dy, int64_t lddy, const void *h, int6
   (void)hipGetLastError();
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   const Rows a{rows, (int)n, weight, param_dtype, 0.0, const_cast<float *>(rstd)};
+  const int64_t blocks = grad_blocks(dtype, sum_dtype, rows, n);
   const int64_t groups = col_groups(dtype, sum_dtype, rows, n), ctiles = col_tiles(dtype, sum_dtype, n);
-  Node *part = reinterpret_cast<Node *>(workspace);
   svm::with_types(dtype, sum_dtype, [&](auto t, auto u) {
     using T = decltype(t);
     using S = decltype(u);
+    constexpr int VE = svm::chunk_values<T, S>();
+    const T *g = (const T *)dy;
+    const S *x = (const S *)h, *d = (const S *)dsum;
+    if (blocks) {
+      float *part = dweight ? reinterpret_cast<float *>(workspace) : nullptr;
+      if (rows > 0)
+        with_tile<VE>(n, [&](auto tl, auto tk, auto tf) {
+          constexpr int L = decltype(tl)::value, K = decltype(tk)::value, FIT = decltype(tf)::value;
+          const auto launch = [&](auto sum) {
+            k_rms_grad<T, S, decltype(sum)::value, L, K, FIT><<<(unsigned)blocks, grad_tpb(L, K * VE, VE), 0, s>>>(
+                g, lddy, x, ldh, d, lddsum, a, (S *)dh, lddh, (T *)dx, lddx, part);
+          };
+          if (dsum) launch(std::true_type{});
+          else launch(std::false_type{});
+        });
+      if (dweight) join_columns(part, rows > 0 ? blocks : 0, n, dweight, param_dtype, s);
+      return;
+    }
+    Node *part = reinterpret_cast<Node *>(workspace);
     if (rows > 0 && (dh || dx))
-      k_rms_dh_any<T, S><<<svm::row_grid(rows), ROW_THREADS, 0, s>>>((const T *)dy, lddy, (const S *)h, ldh, (const S *)dsum,
-                                                                lddsum, a, (S *)dh, lddh, (T *)dx, lddx);
-    if (dweight)
-      k_rms_dw_any<T, S><<<(unsigned)(groups * ctiles), 64 * COL_WAVES, 0, s>>>((const T *)dy, lddy, (const S *)h, ldh,
-                                                                               a, (int)groups, (int)ctiles, part);
+      k_rms_dh_any<T, S><<<svm::row_grid(rows), ROW_THREADS, 0, s>>>(g, lddy, x, ldh, d, lddsum, a, (S *)dh, lddh,
+                                                                     (T *)dx, lddx);
+    if (dweight) {
+      k_rms_dw_any<T, S><<<(unsigned)(groups * ctiles), 64 * COL_WAVES, 0, s>>>(g, lddy, x, ldh, a, (int)groups,
+                                                                               (int)ctiles, part);
+      join_columns(part, groups, n, dweight, param_dtype, s);
+    }
   });
-  if (dweight)
-    svh::in_batches((n + 63) / 64, 1, 64 * JOIN_WAVES, [&](int64_t b0, int64_t blocks) {
-      k_rms_join<<<(unsigned)blocks, 64 * JOIN_WAVES, 0, s>>>(part, (int)groups, (int)n, (int)b0, dweight, param_dtype);
-    });
   return check_launch(who);
 }
 
