@@ -216,6 +216,7 @@ __device__ __forceinline__ void put_fp8(uint8_t *p, int count, const float (&f)[
 constexpr int ROW_THREADS = 512;
 constexpr int64_t ROW_GRID = 8192;  // workgroups of a row launch, at most
 constexpr int BLOCK = 128;          // values that share a scale
+constexpr int64_t LAST_LEVEL = (int64_t)256 << 20;  // bytes of the last-level cache
 
 // Values of one chunk of threads that hold T and S side by side: 16 bytes of
 // the wider type.

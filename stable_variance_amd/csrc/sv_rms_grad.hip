@@ -32,9 +32,14 @@ constexpr int64_t GRAD_RUN = 32;
 // chunks per thread: dy, h and (SUM) dsum are read once, one cross-thread sum
 // per row gives c.  The column sums of the rows a group passes stay in
 // registers; at the end the workgroup's groups are added up through LDS into
-// its row of `part`, [gridDim.x][n] (part == nullptr: not asked for).  What is
-// written is stored non-temporal.
-template <class T, class S, bool SUM, int L, int K, int FIT>
+// its row of `part`, [gridDim.x][n] (part == nullptr: not asked for).
+// STREAM: what is read is loaded non-temporal, which leaves the last-level
+// cache to dh and its reader.  Measured between kernels that write dsum, dy
+// (with 256 MB of other stores between) and one that reads dh, n = 4096 bf16, all
+// of it in us: 4096 rows (100 MB in) 103 with plain loads, 106 so; 8192 rows 164 and
+// 153; 16384 rows 281 and 253.  The kernel alone with its join: 16384 rows 105 and
+// 92 us, 5.9 TB/s.
+template <class T, class S, bool SUM, bool STREAM, int L, int K, int FIT>
 __global__ __launch_bounds__(grad_tpb(L, K * svm::chunk_values<T, S>(), svm::chunk_values<T, S>())) void k_rms_grad(
     const T *__restrict__ dy, int64_t lddy, const S *__restrict__ h, int64_t ldh, const S *__restrict__ dsum,
     int64_t ldds, Rows a, S *__restrict__ dh, int64_t lddh, T *__restrict__ dx, int64_t lddx,
@@ -70,9 +75,9 @@ __global__ __launch_bounds__(grad_tpb(L, K * svm::chunk_values<T, S>(), svm::chu
   int64_t rl = R == 1 || r < rows ? r : rows - 1;  // the row that is loaded
   float rs_next;
   const auto load = [&](int l) {
-    TS::load(h + rl * ldh, n, TS::avail(rows, rl, ldh, n), l, rh);
-    TT::load(dy + rl * lddy, n, TT::avail(rows, rl, lddy, n), l, rg);
-    if constexpr (SUM) TS::load(dsum + rl * ldds, n, TS::avail(rows, rl, ldds, n), l, rd);
+    TS::template load<STREAM>(h + rl * ldh, n, TS::avail(rows, rl, ldh, n), l, rh);
+    TT::template load<STREAM>(dy + rl * lddy, n, TT::avail(rows, rl, lddy, n), l, rg);
+    if constexpr (SUM) TS::template load<STREAM>(dsum + rl * ldds, n, TS::avail(rows, rl, ldds, n), l, rd);
     rs_next = a.rstd[rl];
   };
   const auto arrived = [&] {
@@ -119,11 +124,11 @@ __global__ __launch_bounds__(grad_tpb(L, K * svm::chunk_values<T, S>(), svm::chu
     if constexpr (!FEW) arrived();
     if (own && dh) {
 #pragma unroll
-      for (int k = 0; k < K; ++k) TS::template store_chunk<true>(dh + r * lddh, n, l, k, v);
+      for (int k = 0; k < K; ++k) TS::store_chunk(dh + r * lddh, n, l, k, v);
     }
     if (own && dx) {
 #pragma unroll
-      for (int k = 0; k < K; ++k) TT::template store_chunk<true>(dx + r * lddx, n, l, k, v);
+      for (int k = 0; k < K; ++k) TT::store_chunk(dx + r * lddx, n, l, k, v);
     }
     if constexpr (FEW) {
       __builtin_amdgcn_sched_barrier(0);
@@ -390,15 +395,24 @@ sv_status sv_rms_norm_backward(const void *dy, int64_t lddy, const void *h, int6
     const S *x = (const S *)h, *d = (const S *)dsum;
     if (blocks) {
       float *part = dweight ? reinterpret_cast<float *>(workspace) : nullptr;
+      const bool stream = rows * n * (int64_t)(sizeof(T) + (d ? 2 : 1) * sizeof(S)) > svm::LAST_LEVEL / 4 * 3;
       if (rows > 0)
         with_tile<VE>(n, [&](auto tl, auto tk, auto tf) {
           constexpr int L = decltype(tl)::value, K = decltype(tk)::value, FIT = decltype(tf)::value;
-          const auto launch = [&](auto sum) {
-            k_rms_grad<T, S, decltype(sum)::value, L, K, FIT><<<(unsigned)blocks, grad_tpb(L, K * VE, VE), 0, s>>>(
-                g, lddy, x, ldh, d, lddsum, a, (S *)dh, lddh, (T *)dx, lddx, part);
+          const auto rows_of = [&](auto sum, auto st) {
+            k_rms_grad<T, S, decltype(sum)::value, decltype(st)::value, L, K, FIT>
+                <<<(unsigned)blocks, grad_tpb(L, K * VE, VE), 0, s>>>(g, lddy, x, ldh, d, lddsum, a, (S *)dh, lddh,
+                                                                      (T *)dx, lddx, part);
           };
-          if (dsum) launch(std::true_type{});
-          else launch(std::false_type{});
+          const auto launch = [&](auto st) {
+            if (dsum) rows_of(std::true_type{}, st);
+            else rows_of(std::false_type{}, st);
+          };
+          // rows of whole chunks only: the others are bound by more than the read
+          if constexpr (FIT == svr::FIT_CHUNKS) {
+            if (stream) return launch(std::true_type{});
+          }
+          launch(std::false_type{});
         });
       if (dweight) join_columns(part, rows > 0 ? blocks : 0, n, dweight, param_dtype, s);
       return;

@@ -153,7 +153,8 @@ struct RowTile {
   // outside the row, the row's first chunk is loaded instead (load_rest brings
   // what is missing).  So every thread loads K chunks on every path
   // and the compiler can leave later loads in flight when it waits for these:
-  // a load under a condition makes it wait for all.
+  // a load under a condition makes it wait for all.  NT: non-temporal.
+  template <bool NT = false>
   __device__ static __forceinline__ void load(const T *__restrict__ p, int n, int avail, int l, Vec (&raw)[K]) {
     if constexpr (FIT == FIT_SMALL) return;
 #pragma unroll
@@ -163,7 +164,12 @@ struct RowTile {
         const bool ok = FIT == FIT_ANY ? e < n && e + VE <= avail : e < n;
         e = ok ? e : 0;  // avail >= n >= VE
       }
-      __builtin_memcpy(&raw[k], p + e, sizeof(Vec));
+      if constexpr (NT) {
+        typedef Vec Unaligned __attribute__((aligned(sizeof(T))));
+        raw[k] = __builtin_nontemporal_load(reinterpret_cast<const Unaligned *>(p + e));
+      } else {
+        __builtin_memcpy(&raw[k], p + e, sizeof(Vec));
+      }
     }
   }
 
