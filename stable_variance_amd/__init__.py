@@ -33,7 +33,7 @@ import ctypes
 import os
 import threading
 
-from .build import LIB as _LIB_PATH
+from .build import LIB as _LIB_PATH, MODULE as _MODULE_PATH
 
 __all__ = ["tree_sum", "var", "var_variant", "capi", "library_path", "SvError", "set_tuning", "VARIANTS",
            "layer_norm", "layer_norm_backward", "rms_norm", "rms_norm_fp8", "rms_norm_backward", "embedding",
@@ -153,6 +153,26 @@ def capi():
                 L.sv_probe_read_bandwidth.argtypes = [vp, i64, vp, vp]
                 _lib = L
     return _lib
+
+
+_native = None
+
+
+def native():
+    """The module sv_torch, the short way from ordinary tensors to the library
+    (raises if absent)."""
+    global _native
+    if _native is None:
+        import importlib.util
+
+        capi()  # loads torch and the library
+        if not os.path.exists(_MODULE_PATH):
+            raise ImportError(f"sv_torch.so is not built ({_MODULE_PATH}); run __graft_entry__.build()")
+        spec = importlib.util.spec_from_file_location("sv_torch", _MODULE_PATH)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        _native = module
+    return _native
 
 
 def _check(status: int) -> None:

@@ -1,4 +1,5 @@
-"""Build libstable_variance.so for gfx950 with hipcc (in-tree, no JIT cache)."""
+"""Build libstable_variance.so for gfx950 with hipcc, and the module sv_torch
+that passes torch's tensors to it, with g++ (both in-tree, no JIT cache)."""
 from __future__ import annotations
 
 import os
@@ -17,8 +18,10 @@ DEPS = SRCS + [os.path.join(HERE, "csrc", "sv_device.hpp"), os.path.join(HERE, "
                os.path.join(HERE, "csrc", "sv_rows.hpp"), os.path.join(HERE, "csrc", "sv_rms.hpp"),
                os.path.join(HERE, "csrc", "sv_rms_rows.hpp"),
                os.path.join(ROOT, "include", "stable_variance.h")]
+MODULE_SRC = os.path.join(HERE, "csrc", "sv_torch.cpp")
 OUT_DIR = os.path.join(HERE, "_lib")
 LIB = os.path.join(OUT_DIR, "libstable_variance.so")
+MODULE = os.path.join(OUT_DIR, "sv_torch.so")
 
 # -ffp-contract=off and no fast-math keep every TwoSum operation rounded on
 # its own; packed FP32 instructions are disabled for the device code.
@@ -37,11 +40,34 @@ def hipcc() -> str:
     return "hipcc"
 
 
+def module_commands(obj: str, out: str):
+    """The compile and the link command of the module; the link needs LIB."""
+    import sysconfig
+
+    import torch
+
+    root = os.path.dirname(torch.__file__)
+    dirs = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+            os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(hipcc()))), "include"),
+            sysconfig.get_paths()["include"]]
+    cxx = ["g++", "-O2", "-std=c++17", "-fPIC", "-Wall", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
+    for d in dirs:
+        cxx += ["-isystem", d]
+    link = ["g++", "-shared", obj, "-L" + OUT_DIR, "-l:" + os.path.basename(LIB), "-L" + os.path.join(root, "lib"),
+            "-lc10", "-lc10_hip", "-ltorch_cpu", "-ltorch_python", "-Wl,-rpath,$ORIGIN", "-o", out]
+    return [*cxx, "-c", MODULE_SRC, "-o", obj], link
+
+
 def build(verbose: bool = False) -> str:
-    """Compile the HIP sources (in parallel) and link the shared object; returns its path."""
+    """Compile the sources (in parallel) and link the library and the module; returns the library's path."""
     os.makedirs(OUT_DIR, exist_ok=True)
     flags = [f for f in HIPCC_FLAGS if f != "-shared"]
-    objs, procs = [], []
+    module_obj, module_tmp = os.path.join(OUT_DIR, "sv_torch.o"), MODULE + ".tmp"
+    compile_module, link_module = module_commands(module_obj, module_tmp)
+    objs = []
+    procs = [(compile_module, subprocess.Popen(compile_module, stdout=subprocess.PIPE, stderr=subprocess.PIPE,
+                                               text=True))]
     for src in SRCS:
         obj = os.path.join(OUT_DIR, os.path.splitext(os.path.basename(src))[0] + ".o")
         cmd = [hipcc(), *flags, "-c", src, "-o", obj]
@@ -64,16 +90,22 @@ def build(verbose: bool = False) -> str:
     if verbose:
         print(" ".join(cmd))
     os.replace(tmp, LIB)
-    for obj in objs:
+    res = subprocess.run(link_module, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError("link failed:\n" + " ".join(link_module) + "\n" + res.stdout + res.stderr)
+    if verbose:
+        print(" ".join(link_module))
+    os.replace(module_tmp, MODULE)
+    for obj in [*objs, module_obj]:
         os.remove(obj)
     return LIB
 
 
 def is_stale() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(MODULE):
         return True
-    t = os.path.getmtime(LIB)
-    return any(os.path.getmtime(d) > t for d in DEPS)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(MODULE))
+    return any(os.path.getmtime(d) > t for d in [*DEPS, MODULE_SRC])
 
 
 if __name__ == "__main__":

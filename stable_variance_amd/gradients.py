@@ -13,8 +13,9 @@ import ctypes
 from operator import attrgetter
 
 import torch
+from torch.autograd import forward_ad
 
-from . import SvError, _check, capi
+from . import SvError, _check, capi, native
 from .layers import _CODES, _no_tangents, _on, _raw_stream, _stored, _TYPES, _UNSUPPORTED
 
 __all__ = ["grad_norm", "clip_grad_norm"]
@@ -85,6 +86,10 @@ def grad_norm(grads):
     densely is copied first.  The same list of sizes and types gives the same
     bits on every run.
     """
+    if forward_ad._current_level < 0:
+        norm = native().grad_norm(grads)  # None for other than ordinary tensors
+        if norm is not None:
+            return norm
     ts = _tensors(grads, "grads")
     device = ts[0].device
     ts = [t if _dense(t) and not t.is_neg() else _stored(t) for t in ts]
@@ -109,9 +114,13 @@ def clip_grad_norm(grads, max_norm: float, out=None):
     norm that is Inf or NaN raises nothing: with Inf every finite value becomes
     0 and an Inf becomes NaN, with NaN all values do.
     """
+    max_norm = float(max_norm)
+    if forward_ad._current_level < 0:
+        result = native().clip_grad_norm(grads, max_norm, out)  # None for other than ordinary tensors
+        if result is not None:
+            return result
     ts = _tensors(grads, "grads")
     device = ts[0].device
-    max_norm = float(max_norm)
     if out is None:
         with _on(device):
             outs = [torch.empty_like(t, memory_format=torch.contiguous_format) for t in ts]

@@ -25,7 +25,7 @@ import operator
 import torch
 from torch.autograd import forward_ad
 
-from . import SvError, _check, capi
+from . import SvError, _check, capi, native
 
 __all__ = ["layer_norm", "layer_norm_backward", "rms_norm", "rms_norm_fp8", "rms_norm_backward", "embedding",
            "embedding_backward"]
@@ -236,6 +236,14 @@ _FP8 = {torch.float8_e4m3fn: 3, torch.float8_e5m2: 4}
 _BLOCK = 128  # values that share a scale
 
 
+def _short(x, weight, eps, residual, want_rstd, out_code=0, block=0):
+    """The call for ordinary tensors (contiguous, on the current device, nothing
+    to record), None for others."""
+    if forward_ad._current_level >= 0:
+        return None
+    return native().rms(x, weight, residual, eps, want_rstd, out_code, block)
+
+
 def _rms_inputs(x, weight, residual, rows, n):
     """Checked and stored: x, its row stride, the residual, its row stride and
     type code, the weight and its type."""
@@ -284,8 +292,8 @@ class _RmsNorm(torch.autograd.Function):
         if dy is None:  # y took no part
             dx = dsum.to(ctx.x_dtype) if need_x and dsum is not None else None
             return dx, None, dsum if need_r else None, None
-        dh, dx, dw = _rms_backward(dy, h, rstd, weight, dsum, need_r or (need_x and not mixed), need_x and mixed, need_w,
-                                   weight.dtype if weight is not None else None)
+        args = dy, h, rstd, weight, dsum, need_r or (need_x and not mixed), need_x and mixed, need_w
+        dh, dx, dw = _short_backward(*args) or _rms_backward(*args, weight.dtype if weight is not None else None)
         return dx if mixed else dh if need_x else None, dw, dh if need_r else None, None
 
 
@@ -302,9 +310,12 @@ def rms_norm(x, weight=None, eps: float = 1e-6, residual=None, return_rstd: bool
     strided; a last dimension that is not contiguous is copied first.  A row's
     result does not depend on the other rows.
     """
+    eps = float(eps)
+    out = _short(x, weight, eps, residual, return_rstd)
+    if out is not None:
+        return out
     _tensor(x, "x", _TYPES)
     _no_tangents(x, weight, residual)
-    eps = float(eps)
     # what is no tensor is refused where the other arguments are checked
     if torch.is_grad_enabled() and (x.requires_grad or getattr(weight, "requires_grad", False)
                                     or getattr(residual, "requires_grad", False)):
@@ -330,14 +341,18 @@ def rms_norm_fp8(x, weight=None, eps: float = 1e-6, residual=None, dtype=torch.f
     enabled.  A training step calls it under ``torch.no_grad()`` and
     ``rms_norm_backward`` with the ``h`` (or x) and ``rstd`` it left.
     """
-    _tensor(x, "x", _TYPES)
-    _no_tangents(x, weight, residual)
-    if torch.is_grad_enabled() and any(getattr(t, "requires_grad", False) for t in (x, weight, residual)):
-        raise NotImplementedError("rms_norm_fp8 has no gradient: call it under torch.no_grad()")
     if dtype not in _FP8:
         raise TypeError(f"dtype must be {' or '.join(str(d) for d in _FP8)}, got {dtype}")
     if block is not None and (isinstance(block, bool) or operator.index(block) != _BLOCK):
         raise ValueError(f"block must be {_BLOCK}, or None for whole rows, got {block}")
+    eps = float(eps)
+    out = _short(x, weight, eps, residual, return_rstd, _FP8[dtype], 0 if block is None else _BLOCK)
+    if out is not None:
+        return out
+    _tensor(x, "x", _TYPES)
+    _no_tangents(x, weight, residual)
+    if torch.is_grad_enabled() and any(getattr(t, "requires_grad", False) for t in (x, weight, residual)):
+        raise NotImplementedError("rms_norm_fp8 has no gradient: call it under torch.no_grad()")
     rows, n = _shape_2d(x, "x")
     x2, ldx, r2, ldr, sum_code, w = _rms_inputs(x, weight, residual, rows, n)
     code = _CODES[x.dtype]
@@ -347,10 +362,17 @@ def rms_norm_fp8(x, weight=None, eps: float = 1e-6, residual=None, dtype=torch.f
         h = None if residual is None else torch.empty_like(residual, memory_format=torch.contiguous_format)
         rstd = x.new_empty(x.shape[:-1], dtype=torch.float32) if return_rstd else None
         _check(capi().sv_rms_norm_fp8(_ptr(x2), ldx, _ptr(r2), ldr, code, sum_code, rows, n, _ptr(w),
-                                      code if w is None else _CODES[w.dtype], float(eps), _FP8[dtype],
+                                      code if w is None else _CODES[w.dtype], eps, _FP8[dtype],
                                       0 if block is None else _BLOCK, _ptr(q), n, _ptr(scale), _ptr(h), n, _ptr(rstd),
                                       _raw_stream(x.device.index)))
     return (q, scale) + (() if h is None else (h,)) + (() if rstd is None else (rstd,))
+
+
+def _short_backward(*args):
+    """As _short for the backward pass, with a weight."""
+    if forward_ad._current_level >= 0:
+        return None
+    return native().rms_backward(*args)
 
 
 def _rms_backward(dy, h, rstd, weight, dsum, need_dh, need_dx, need_w, param_dtype):
@@ -386,6 +408,10 @@ def rms_norm_backward(dy, h, rstd, weight=None, dsum=None, *, weight_grad: bool 
     when there is no weight; float32 by default) and is None where not asked
     for.
     """
+    if weight is not None and param_dtype in (None, getattr(weight, "dtype", None)):
+        out = _short_backward(dy, h, rstd, weight, dsum, True, False, bool(weight_grad))
+        if out is not None:
+            return out[0], out[2]
     _tensor(dy, "dy", _TYPES)
     _tensor(h, "h", (dy.dtype, torch.float32) if dy.dtype != torch.float32 else (torch.float32,))
     _same_device(h, dy, "dy")

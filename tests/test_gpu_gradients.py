@@ -418,3 +418,64 @@ def test_c_abi_row_strides_leave_the_gaps_alone(dev):
                 assert torch.equal(wh[:, :n], dh) and (wh[:, n:] == 7).all(), (n, gap)
                 assert torch.equal(wy[:, :n], dh.to(dtype))  # dh is the float32 value, or in the same type
                 assert (wy[:, n:] == 7).all(), (n, gap)
+
+
+# ---------------------------------------------------------------- the two ways into the library
+
+def test_both_ways_give_the_same(dev, monkeypatch):
+    from test_gpu_rms import general_way
+
+    sets = [tensors([5, 0, 4097, 100003], TYPES, 1), tensors([300] * 200, [BF16, F32], 2),
+            [t.reshape(-1, 1) for t in tensors([64, 33], [F16], 3)]]
+    short = []
+    for ts in sets:
+        mine = [t.clone() for t in ts]
+        outs = [torch.empty_like(t) for t in ts]
+        short.append([sv.grad_norm(ts), sv.grad_norm(tuple(ts)), *sv.clip_grad_norm(ts, 0.2)[0],
+                      *sv.clip_grad_norm(ts, 0.2, out=outs)[0], *sv.clip_grad_norm(mine, 0.2, out=mine)[0],
+                      sv.clip_grad_norm(ts, 0.2)[1]])
+        got = sv.clip_grad_norm(ts, 0.2, out=outs)[0]
+        assert type(got) is list and all(p is q for p, q in zip(got, outs))
+    general_way(monkeypatch)
+    for ts, want in zip(sets, short):
+        mine = [t.clone() for t in ts]
+        outs = [torch.empty_like(t) for t in ts]
+        got = [sv.grad_norm(ts), sv.grad_norm(iter(ts)), *sv.clip_grad_norm(ts, 0.2)[0],
+               *sv.clip_grad_norm(ts, 0.2, out=outs)[0], *sv.clip_grad_norm(mine, 0.2, out=mine)[0],
+               sv.clip_grad_norm(ts, 0.2)[1]]
+        assert len(got) == len(want)
+        assert all(p.shape == q.shape and p.dtype == q.dtype and torch.equal(p, q) for p, q in zip(got, want))
+
+
+def test_general_way_refuses_and_converts_too(dev, monkeypatch):
+    from test_gpu_rms import general_way
+
+    general_way(monkeypatch)
+    test_refusals(dev)
+    test_in_place_counts_as_a_write(dev)
+    test_zero_nan_and_inf(dev)
+    test_strides(dev)
+    test_neighbours_stay(dev)
+
+
+def test_the_short_way_leaves_the_others(dev):
+    from stable_variance_amd import native
+
+    m = native()
+    a, b = torch.ones(100, device=dev), torch.ones(4, 5, device=dev)
+    assert m.grad_norm([a, b]) is not None and m.grad_norm((a,)) is not None
+    for bad in ([], (), iter([a]), a, None, [a, None], [a, b.t()], [a.cpu()], [a, a.double()], [a.to_sparse()],
+                [a[::2]], [torch._neg_view(a)], [1.0]):
+        assert m.grad_norm(bad) is None
+        assert m.clip_grad_norm(bad, 1.0, None) is None
+    c = a.clone()
+    for out in ([], [c, c], [b], [c.to(BF16)], [c.cpu()], [c[:50]], c, [c.requires_grad_()]):
+        assert m.clip_grad_norm([a], 1.0, out) is None
+    for most in (-1.0, float("nan")):
+        assert m.clip_grad_norm([a], most, None) is None
+    assert m.clip_grad_norm([a, a], 1.0, [a, a]) is None  # written twice
+    assert (a == 1).all()
+    with pytest.raises(TypeError):
+        m.clip_grad_norm([a], "x", None)
+    with pytest.raises(TypeError):
+        m.clip_grad_norm([a], 1.0)

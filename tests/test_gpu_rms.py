@@ -584,3 +584,138 @@ def test_refusals(dev):
             sv.rms_norm(x, eps=eps)
         with pytest.raises(sv.SvError):
             sv.rms_norm_fp8(x, eps=eps)
+
+
+# ---------------------------------------------------------------- the two ways into the library
+
+class NoModule:
+    """Stands in for the short way: every call takes the general one."""
+
+    @staticmethod
+    def rms(*_):
+        return None
+
+    rms_backward = grad_norm = clip_grad_norm = rms
+
+
+def general_way(monkeypatch):
+    from stable_variance_amd import gradients, layers
+
+    for module in (layers, gradients):
+        monkeypatch.setattr(module, "native", lambda: NoModule)
+
+
+def test_both_ways_give_the_same(dev, monkeypatch):
+    calls = []
+    for dtype, stream in STREAMS:
+        for shape in ((5, 136), (2, 3, 40), (4096,), (3, 1531)):
+            n = shape[-1]
+            x = hidden(math.prod(shape[:-1]), n, dtype, 1).reshape(shape)
+            r = None if stream is None else hidden(math.prod(shape[:-1]), n, stream, 2).reshape(shape)
+            for w in (None, weights(n, dtype, 3), weights(n, F32, 4)):
+                for rstd in (False, True):
+                    calls.append((lambda x=x, w=w, r=r, rstd=rstd: sv.rms_norm(x, w, 0.01, r, rstd)))
+                    for to, block in ((E4M3, 128), (E5M2, None)):
+                        calls.append((lambda x=x, w=w, r=r, rstd=rstd, to=to, block=block:
+                                      sv.rms_norm_fp8(x, w, 0.01, r, to, block, rstd)))
+    from stable_variance_amd import native
+
+    real, taken = native(), []
+
+    class Counted:
+        @staticmethod
+        def rms(*args):
+            out = real.rms(*args)
+            taken.append(out is not None)
+            return out
+
+    from stable_variance_amd import layers
+
+    with monkeypatch.context() as m:
+        m.setattr(layers, "native", lambda: Counted)
+        short = [c() for c in calls]
+    assert taken == [True] * len(calls)
+    general_way(monkeypatch)
+    for a, c in zip(short, calls):
+        b = c()
+        assert type(a) is type(b)
+        a, b = (a, b) if isinstance(a, tuple) else ((a,), (b,))
+        assert len(a) == len(b)
+        for p, q in zip(a, b):
+            assert p.dtype == q.dtype and p.shape == q.shape and p.device == q.device and not p.requires_grad
+            assert torch.equal(p.reshape(-1).view(torch.uint8), q.reshape(-1).view(torch.uint8))
+
+
+def test_both_ways_back_give_the_same(dev, monkeypatch):
+    from stable_variance_amd import layers
+
+    calls, short = [], []
+    for dtype, stream in PAIRS:
+        for shape in ((5, 136), (2, 3, 40), (4096,), (3, 1531)):
+            n, rows = shape[-1], math.prod(shape[:-1])
+            h, dy, dsum = (hidden(rows, n, t, i).reshape(shape) for i, t in enumerate((stream, dtype, stream)))
+            rstd = sv.rms_norm(h, return_rstd=True)[1]
+            for w in (weights(n, dtype, 3), weights(n, F32, 4)):
+                for d in (None, dsum):
+                    for dw in (True, False):
+                        calls.append((dy, h, rstd, w, d, dw))
+    for dy, h, rstd, w, d, dw in calls:
+        out = layers._short_backward(dy, h, rstd, w, d, True, True, dw)
+        assert out is not None
+        assert torch.equal(out[1], out[0].to(dy.dtype))
+        short.append(sv.rms_norm_backward(dy, h, rstd, w, d, weight_grad=dw))
+        assert torch.equal(short[-1][0], out[0])
+    general_way(monkeypatch)
+    for (dy, h, rstd, w, d, dw), want in zip(calls, short):
+        got = sv.rms_norm_backward(dy, h, rstd, w, d, weight_grad=dw)
+        for p, q in zip(got, want):
+            assert p is q is None or (p.dtype == q.dtype and torch.equal(p, q) and not q.requires_grad)
+    test_autograd(dev)
+    test_refusals(dev)
+
+
+def test_the_short_way_back_leaves_the_others(dev):
+    from stable_variance_amd import native
+
+    m = native()
+    dy, h, rstd, w, d = hidden(4, 8, BF16, 1), hidden(4, 8, F32, 2), torch.ones(4, device=dev), weights(8, F32, 1), \
+        hidden(4, 8, F32, 3)
+    ok = (dy, h, rstd, w, d, True, False, True)
+    assert m.rms_backward(*ok) is not None
+    for i, bad in ((0, dy.cpu()), (0, dy.double()), (0, dy[:3]), (0, dy.t()), (0, None), (0, dy.to(F16)[:, ::2]), (1, h[:3]),
+                   (1, h.to(F16)), (1, h.t()), (1, h[0, 0]), (1, h.cpu()), (2, rstd[:3]), (2, rstd[:, None]),
+                   (2, rstd.to(BF16)), (2, rstd.cpu()), (3, None), (3, w[:7]), (3, w.to(F16)), (3, w[None]), (4, d[:3]),
+                   (4, d.to(BF16)), (4, d.cpu()), (4, torch._neg_view(d)), (4, 1.0)):
+        args = list(ok)
+        args[i] = bad
+        assert m.rms_backward(*args) is None, (i, bad)
+    assert m.rms_backward(dy[:0], h[:0], rstd[:0], *ok[3:]) is None
+    with pytest.raises(TypeError):
+        m.rms_backward(*ok[:7])
+
+
+def test_the_short_way_leaves_the_others(dev):
+    from stable_variance_amd import native
+
+    m = native()
+    x, w, r = hidden(4, 8, BF16, 1), weights(8, F32, 1), hidden(4, 8, F32, 2)
+    ok = (x, w, r, 1e-6, False, 0, 0)
+    assert m.rms(*ok) is not None
+    half_view = torch.randn(4, 8, dtype=torch.complex64, device=dev).conj().imag
+    for i, bad in ((0, x.cpu()), (0, x.double()), (0, x[:, ::2]), (0, x.t()), (0, x[:0]), (0, x[:, :0]), (0, x[0, 0]),
+                   (0, 1.0), (0, None), (0, x.to_sparse()), (0, half_view), (0, torch._neg_view(x)),
+                   (0, x.clone().requires_grad_()), (1, w.clone().requires_grad_()), (2, r.clone().requires_grad_()),
+                   (1, w[:7]), (1, w[None]), (1, w.to(F16)), (1, w.cpu()), (1, w.double()), (1, [1.0] * 8),
+                   (2, r[:3]), (2, r.to(F16)), (2, r.cpu()), (2, r.t()), (2, r.reshape(2, 2, 8)), (2, 0.5),
+                   (3, -1.0), (3, float("nan"))):
+        args = list(ok)
+        args[i] = bad
+        assert m.rms(*args) is None, (i, bad)
+    with torch.no_grad():
+        assert m.rms(x.clone().requires_grad_(), *ok[1:]) is not None
+    p = torch.nn.Parameter(w)
+    with torch.no_grad():
+        assert m.rms(x, p, *ok[2:]) is not None
+    for args in ((), (x,), ok + (1,), (x, w, r, "a", False, 0, 0)):
+        with pytest.raises(TypeError):
+            m.rms(*args)
