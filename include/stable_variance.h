@@ -499,7 +499,7 @@ sv_status sv_rms_norm(const void *x, int64_t ldx, const void *residual, int64_t 
  * of a row (128; the row's last block may be shorter) or, with block == 0,
  * for each whole row, with y_i in float32 as above:
  *   scale = max(max|y_i| / M, 2^-126),  M = 448 (E4M3) or 57344 (E5M2)
- *   q_i = y_i * (1 / scale), cut to [-M, M] and rounded once to out_dtype
+ *   q_i = y_i * (1 / scale), rounded once to out_dtype
  * so that q_i * scale stands for y_i.  An Inf among a block's values makes its
  * scale Inf, its own q NaN and the others 0; a NaN makes both NaN.
  *   q          [rows, n] bytes, row stride ldq

@@ -184,13 +184,10 @@ __device__ __forceinline__ float fp8_scale(unsigned most, bool e5m2) {
 }
 
 // Two values of 8 bits in the low half of a word, from float32 values (round
-// to nearest even).  The product with the scale's reciprocal can pass the
-// largest value by its rounding, which the 8-bit types would make a NaN or
-// Inf, so it is cut there; a NaN stays.
+// to nearest even).  The product with the scale's reciprocal passes the
+// largest value by 2^-22 of it at most, which still rounds to it: the next step
+// would begin at 464 of 448, or 61440 of 57344.
 __device__ __forceinline__ unsigned fp8_pair(float a, float b, bool e5m2) {
-  const float m = fp8_largest(e5m2);
-  a = a > m ? m : a < -m ? -m : a;
-  b = b > m ? m : b < -m ? -m : b;
   return (unsigned)(e5m2 ? __builtin_amdgcn_cvt_pk_bf8_f32(a, b, 0, false)
                          : __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false)) & 0xffffu;
 }

@@ -58,15 +58,6 @@ __global__ __launch_bounds__(grad_tpb(L, K * svm::chunk_values<T, S>(), svm::chu
   const float inv_n = 1.0f / (float)n;
   float wv[FEW ? 1 : K][VE], aw[E];
 #pragma unroll
-  for (int k = 0; k < K; ++k) {
-    const int e = TT::first(l0, k), left = n - e;
-    svm::get_weight<VE>(a.w, a.pt, e, left < 0 ? 0 : left, wv[FEW ? 0 : k]);
-    if constexpr (FEW) {
-#pragma unroll
-      for (int i = 0; i < VE; ++i) wlds[e + i] = wv[0][i];
-    }
-  }
-#pragma unroll
   for (int i = 0; i < E; ++i) aw[i] = 0.0f;
   const int64_t step = (int64_t)gridDim.x * R;
   typename TS::Vec rh[K], rd[SUM ? K : 1];
@@ -86,6 +77,15 @@ __global__ __launch_bounds__(grad_tpb(L, K * svm::chunk_values<T, S>(), svm::chu
     if constexpr (SUM) TS::arrived(rd);
   };
   load(l0);
+#pragma unroll
+  for (int k = 0; k < K; ++k) {  // in flight beside the first row
+    const int e = TT::first(l0, k), left = n - e;
+    svm::get_weight<VE>(a.w, a.pt, e, left < 0 ? 0 : left, wv[FEW ? 0 : k]);
+    if constexpr (FEW) {
+#pragma unroll
+      for (int i = 0; i < VE; ++i) wlds[e + i] = wv[0][i];
+    }
+  }
   if constexpr (!FEW) arrived();
   int turn = 0;
   for (int64_t r0 = (int64_t)blockIdx.x * R; r0 < rows; r0 += step, r += step, turn ^= 1) {

@@ -134,10 +134,6 @@ __global__ __launch_bounds__(tpb(L)) void k_rms_rows(const T *__restrict__ x, in
     const int e = TX::first(l, k), left = n - e;
     svm::get_weight<VE>(a.w, a.pt, e, left < 0 ? 0 : left, w);
   };
-  if constexpr (HOLD) {
-#pragma unroll
-    for (int k = 0; k < K; ++k) weight(l0, k, wv[k]);
-  }
   const int64_t step = (int64_t)gridDim.x * R;
   typename TX::Vec rx[K];
   typename TS::Vec rr[RES ? K : 1];
@@ -152,7 +148,11 @@ __global__ __launch_bounds__(tpb(L)) void k_rms_rows(const T *__restrict__ x, in
     if constexpr (RES) TS::arrived(rr);
   };
   load(l0);
-  if constexpr (HOLD) arrived();
+  if constexpr (HOLD) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) weight(l0, k, wv[k]);  // in flight beside the first row
+    arrived();
+  }
   int turn = 0;
   for (int64_t r0 = (int64_t)blockIdx.x * R; r0 < rows; r0 += step, r += step, turn ^= 1) {
     int l = l0;  // opaque, so that the addresses of all chunks are not kept in registers across rows
