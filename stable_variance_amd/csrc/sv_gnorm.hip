@@ -48,6 +48,8 @@ struct Table {
   int count;
 };
 
+static_assert(sizeof(Table<true>) <= 4000, "a launch's arguments stay below 4 KB");
+
 __host__ __device__ constexpr int64_t unit_values(int dtype) { return UNIT_BYTES / (dtype == SV_DTYPE_F32 ? 4 : 2); }
 
 // Calls fn(i, lo, hi) for the runs of values [lo, hi) of tensor i that make up

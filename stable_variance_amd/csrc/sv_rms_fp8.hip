@@ -28,7 +28,7 @@ sv_status sv_rms_norm_fp8(const void *x, int64_t ldx, const void *residual, int6
     if (reinterpret_cast<uintptr_t>(scale) % sizeof(float))
       return fail(SV_ERR_INVALID_ARGUMENT, "%s: scale is not aligned to its type", who);
   }
-  if (rows == 0) return ok();
+  if (rows == 0 || (n == 0 && block != 0 && !rstd)) return ok();
   if ((st = check_device()) != SV_OK) return st;
   (void)hipGetLastError();
   forward<true>(x, ldx, residual, ldr, dtype, sum_dtype, Rows{rows, (int)n, weight, param_dtype, eps, rstd}, nullptr, 0,

@@ -110,12 +110,17 @@ constexpr int tpb(int L) { return L <= 128 ? 256 : L; }
 // One sum of squares in double across the group's threads per row.
 // What is read next, y or q, is stored as it comes, so that the last-level
 // cache (256 MB) can serve its reader.  The sum h, which is read only behind
-// the next products, is stored non-temporal, and inputs of more than the
-// cache (STREAM), of which it holds little, are loaded so.  Measured between
-// a kernel that writes x and one that reads y, with h read after 256 MB of
-// other stores, n = 4096 bf16, all of it in us: 4096 rows 96.7 with plain h, 96.1
-// with non-temporal h, 98.7 with loads so too; 16384 rows (268 MB in) 241, 236, 229;
-// 32768 rows 443, 434, 398.
+// the next products, is stored non-temporal, and inputs that are no smaller
+// than the cache (STREAM), of which it holds little, are loaded so.  Measured
+// between a kernel that writes x and one that reads y, with h read after 256
+// MB of other stores, n = 4096 bf16, all of it in us, with h stored plainly,
+// then non-temporal, then the loads so too: 4096 rows 96.7, 96.1, 98.7; 16384
+// rows (256 MB in) 241, 236, 229; 32768 rows 443, 434, 398.
+// Bound by the read and the write: 16384 x 8192 bf16 with a residual to 8 bits
+// 147 us, 6.4 TB/s, 200000 x 128 bf16 17.6 us, 5.8 TB/s (a copy in torch runs
+// at 4.9-5.4).  Short of that, few rows: 5003 x 1531 f16 to 8 bits 9.8 us, 2.3 TB/s, where
+// every wave has one row, whose loads, sums and stores follow each other; one
+// row of 4096 takes 2.8 us.
 template <class T, class S, bool RES, bool Q, bool STREAM, int L, int K, int FIT>
 __global__ __launch_bounds__(tpb(L)) void k_rms_rows(const T *__restrict__ x, int64_t ldx, const S *__restrict__ res,
                                                      int64_t ldr, Rows a, T *__restrict__ y, int64_t ldy,
@@ -290,7 +295,7 @@ void forward(const void *x, int64_t ldx, const void *residual, int64_t ldr, int 
     using S = decltype(u);
     constexpr bool RES = decltype(with_residual)::value;
     constexpr int VE = svm::chunk_values<T, S>();
-    const bool stream = a.rows * a.n * (int64_t)(sizeof(T) + (RES ? sizeof(S) : 0)) > svm::LAST_LEVEL;
+    const bool stream = a.rows * a.n * (int64_t)(sizeof(T) + (RES ? sizeof(S) : 0)) >= svm::LAST_LEVEL;
     const bool held = with_tile<VE, Q ? BLOCK / VE : 1>(a.n, [&](auto tl, auto tk, auto tf) {
       constexpr int L = decltype(tl)::value, K = decltype(tk)::value, TPB = tpb(L), R = TPB / L, FIT = decltype(tf)::value;
       const int64_t blocks = (a.rows + R - 1) / R, most = 256 * (2048 / TPB);
