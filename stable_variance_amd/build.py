@@ -8,11 +8,9 @@ import subprocess
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 SRC = os.path.join(HERE, "csrc", "sv_lib.hip")
-SRCS = [SRC, os.path.join(HERE, "csrc", "sv_adn.hip"), os.path.join(HERE, "csrc", "sv_adn_folds_9_14.hip"),
-        os.path.join(HERE, "csrc", "sv_adn_folds_15_21.hip"), os.path.join(HERE, "csrc", "sv_f64.hip"),
-        os.path.join(HERE, "csrc", "sv_norm.hip"), os.path.join(HERE, "csrc", "sv_embed.hip"),
-        os.path.join(HERE, "csrc", "sv_rms.hip"), os.path.join(HERE, "csrc", "sv_rms_fp8.hip"),
-        os.path.join(HERE, "csrc", "sv_rms_grad.hip"), os.path.join(HERE, "csrc", "sv_gnorm.hip")]
+SRCS = [os.path.join(HERE, "csrc", name) for name in (
+    "sv_gnorm.hip", "sv_f64.hip", "sv_rms.hip", "sv_rms_grad.hip", "sv_embed.hip", "sv_lib.hip", "sv_norm.hip",
+    "sv_rms_fp8.hip", "sv_adn.hip", "sv_adn_folds_9_14.hip", "sv_adn_folds_15_21.hip")]
 DEPS = SRCS + [os.path.join(HERE, "csrc", "sv_device.hpp"), os.path.join(HERE, "csrc", "sv_host.hpp"),
                os.path.join(HERE, "csrc", "sv_index.hpp"), os.path.join(HERE, "csrc", "sv_adn_kernel.hpp"),
                os.path.join(HERE, "csrc", "sv_rows.hpp"), os.path.join(HERE, "csrc", "sv_rms.hpp"),

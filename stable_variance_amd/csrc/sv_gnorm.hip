@@ -100,7 +100,8 @@ __device__ __forceinline__ double sum_squares(const T *p, int64_t n) {
 #pragma unroll
     for (int k = 0; k < BATCH; ++k) v[k] = load_chunk<NT>(q + e + k * STEP);
 #pragma unroll
-    for (int k = 0; k < BATCH; ++k) s[k] += svr::pair_sum<0, VE>([&](int i) { return svm::square(svr::to_f<T>(v[k][i])); });
+    for (int k = 0; k < BATCH; ++k)
+      s[k] += svr::pair_sum<0, VE>([&](int i) { return svm::square(svr::to_f<T>(v[k][i])); });
   }
   for (e += threadIdx.x * VE; e < n; e += STEP) {
     float f[VE];
@@ -113,9 +114,9 @@ __device__ __forceinline__ double sum_squares(const T *p, int64_t n) {
 // The sum of squares of each workgroup's units.  AGAIN: the values are read
 // again soon (clipping), so the loads leave what the caches hold of them; else
 // they are non-temporal.  Eight waves per SIMD (64 registers) with four chunks
-// a thread in flight; bound by the read.  1.74 GB of bf16: 257 us, 6.8 TB/s (plain loads
-// 293 us, 96 registers 269, one chunk in flight 290); a plain read of them
-// takes 247.  100 MB clipped: 51 us with plain loads here, 54 with non-temporal.
+// a thread in flight; bound by the read.  1.74 GB of bf16: 257 us, 6.8 TB/s
+// (plain loads 293 us, 96 registers 269, one chunk in flight 290); a plain read
+// of them takes 247.  100 MB clipped: 51 us with plain loads, 54 with others.
 template <bool AGAIN>
 __global__ __launch_bounds__(THREADS, 8) void k_gnorm_sum(Table<false> t, int64_t units, int64_t per, double *part) {
   __shared__ double lds[THREADS / 64];
@@ -186,8 +187,8 @@ __device__ __forceinline__ void scale_values(const T *p, T *out, int64_t n, floa
 }
 
 // One unit per workgroup, in the order of memory: 1.34 GB of float32 scaled in
-// 404 us, 6.6 TB/s, where 2048 workgroups of 40 units each take 510.  Loads and stores
-// non-temporal (plain stores 475 us, plain loads 465).
+// 404 us, 6.6 TB/s, where 2048 workgroups of 40 units each take 510.  Loads and
+// stores non-temporal (plain stores 475 us, plain loads 465).
 __global__ __launch_bounds__(THREADS) void k_gnorm_scale(Table<true> t, int64_t units, int64_t per,
                                                          const float *factor) {
   const float k = *factor;

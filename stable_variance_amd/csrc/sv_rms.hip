@@ -35,8 +35,8 @@ sv_status sv_rms_norm(const void *x, int64_t ldx, const void *residual, int64_t 
                       int64_t rows, int64_t n, const void *weight, int param_dtype, double eps, void *y, int64_t ldy,
                       void *sum, int64_t ldsum, float *rstd, void *stream) {
   static const char who[] = "sv_rms_norm";
-  sv_status st = svm::check_forward(who, x, ldx, residual, ldr, dtype, sum_dtype, rows, n, weight, param_dtype, eps, sum,
-                               ldsum);
+  sv_status st = svm::check_forward(who, x, ldx, residual, ldr, dtype, sum_dtype, rows, n, weight, param_dtype, eps,
+                                    sum, ldsum);
   if (st != SV_OK) return st;
   if ((st = svr::check_matrix(who, "y", y, ldy, rows, n, svr::dtype_bytes(dtype))) != SV_OK) return st;
   if (rows == 0 || (n == 0 && !rstd)) return ok();

@@ -251,7 +251,8 @@ inline void with_types(int dtype, int sum_dtype, Fn &&fn) {
 
 // Checks that the calls share; SV_OK without touching the message.
 inline sv_status check_rows(const char *who, int dtype, int sum_dtype, int64_t rows, int64_t n, int param_dtype) {
-  if (!svr::dtype_bytes(dtype)) return svh::fail(SV_ERR_INVALID_ARGUMENT, "%s: dtype %d is not a type code", who, dtype);
+  if (!svr::dtype_bytes(dtype))
+    return svh::fail(SV_ERR_INVALID_ARGUMENT, "%s: dtype %d is not a type code", who, dtype);
   if (sum_dtype != dtype && sum_dtype != SV_DTYPE_F32)
     return svh::fail(SV_ERR_INVALID_ARGUMENT, "%s: sum_dtype %d must be dtype or SV_DTYPE_F32", who, sum_dtype);
   if (param_dtype != dtype && param_dtype != SV_DTYPE_F32)
@@ -268,9 +269,9 @@ inline sv_status check_rows(const char *who, int dtype, int sum_dtype, int64_t r
 }
 
 // Checks of the forward calls.
-inline sv_status check_forward(const char *who, const void *x, int64_t ldx, const void *residual, int64_t ldr, int dtype,
-                        int sum_dtype, int64_t rows, int64_t n, const void *weight, int param_dtype, double eps,
-                        const void *sum, int64_t ldsum) {
+inline sv_status check_forward(const char *who, const void *x, int64_t ldx, const void *residual, int64_t ldr,
+                               int dtype, int sum_dtype, int64_t rows, int64_t n, const void *weight, int param_dtype,
+                               double eps, const void *sum, int64_t ldsum) {
   sv_status st = check_rows(who, dtype, sum_dtype, rows, n, param_dtype);
   if (st != SV_OK) return st;
   if (!(eps >= 0.0) || eps > 3.0e38) return svh::fail(SV_ERR_INVALID_ARGUMENT, "%s: eps must be >= 0 and finite", who);

@@ -14,8 +14,8 @@ sv_status sv_rms_norm_fp8(const void *x, int64_t ldx, const void *residual, int6
                           int64_t block, void *q, int64_t ldq, float *scale, void *sum, int64_t ldsum, float *rstd,
                           void *stream) {
   static const char who[] = "sv_rms_norm_fp8";
-  sv_status st = svm::check_forward(who, x, ldx, residual, ldr, dtype, sum_dtype, rows, n, weight, param_dtype, eps, sum,
-                               ldsum);
+  sv_status st = svm::check_forward(who, x, ldx, residual, ldr, dtype, sum_dtype, rows, n, weight, param_dtype, eps,
+                                    sum, ldsum);
   if (st != SV_OK) return st;
   if (out_dtype != SV_DTYPE_E4M3 && out_dtype != SV_DTYPE_E5M2)
     return fail(SV_ERR_INVALID_ARGUMENT, "%s: out_dtype %d must be SV_DTYPE_E4M3 or SV_DTYPE_E5M2", who, out_dtype);

@@ -34,11 +34,13 @@ constexpr int64_t GRAD_RUN = 32;
 // registers; at the end the workgroup's groups are added up through LDS into
 // its row of `part`, [gridDim.x][n] (part == nullptr: not asked for).
 // STREAM: what is read is loaded non-temporal, which leaves the last-level
-// cache to dh and its reader.  Measured between kernels that write dsum, dy
-// (with 256 MB of other stores between) and one that reads dh, n = 4096 bf16, all
-// of it in us: 4096 rows (100 MB in) 103 with plain loads, 106 so; 8192 rows 164 and
-// 153; 16384 rows 281 and 253.  The kernel alone with its join: 16384 rows 105 and
-// 92 us, 5.9 TB/s.
+// cache to dh and its reader.  Measured between kernels that write dsum and dy
+// (with 256 MB of other stores between) and one that reads dh, n = 4096 bf16,
+// all of it in us, with plain loads and so: 4096 rows (100 MB in) 103 and 106;
+// 8192 rows 164 and 153; 16384 rows 281 and 253.
+// Bound by the three or four streams: 16384 x 4096 bf16 with dsum 89 us and 5
+// for the join, 6.1 TB/s.  5003 x 1531 f16 16 us, 3.0 TB/s: 2.4 rounds of rows
+// over the chip, two waves per SIMD.
 template <class T, class S, bool SUM, bool STREAM, int L, int K, int FIT>
 __global__ __launch_bounds__(grad_tpb(L, K * svm::chunk_values<T, S>(), svm::chunk_values<T, S>())) void k_rms_grad(
     const T *__restrict__ dy, int64_t lddy, const S *__restrict__ h, int64_t ldh, const S *__restrict__ dsum,
@@ -151,9 +153,13 @@ __global__ __launch_bounds__(grad_tpb(L, K * svm::chunk_values<T, S>(), svm::chu
 }
 
 // Calls fn(L, K, FIT) (integral constants) with the smallest tile of VE-value
-// chunks that holds n values; false when none does.
+// chunks that holds n values; false when none does.  Rows of whole chunks have
+// kernels of their own only for 1024 threads, where no register is left for the
+// others, and (`whole`) for inputs that are loaded non-temporal: elsewhere they
+// gain up to 4% (4096 x 4096 bf16 22.6 against 23.6 us) and with the forward
+// pass's that would be a third of the library.
 template <int VE, class Fn>
-bool with_tile(int64_t n, Fn &&fn) {
+bool with_tile(int64_t n, bool whole, Fn &&fn) {
   if (n < 1) return false;
   const auto tile = [&](auto tl, auto tk) {
     constexpr int L = decltype(tl)::value, K = decltype(tk)::value;
@@ -164,17 +170,18 @@ bool with_tile(int64_t n, Fn &&fn) {
       }
     }
     if (n > (int64_t)L * K * VE) return false;
-    constexpr bool WHOLE = L > 512;  // whole chunks only: no register is left for the others
-    if (n % VE == 0) {
-      fn(tl, tk, std::integral_constant<int, svr::FIT_CHUNKS>{});
-      return true;
+    if constexpr (L >= 128) {
+      if (n % VE == 0 && (L > 512 || whole)) {
+        fn(tl, tk, std::integral_constant<int, svr::FIT_CHUNKS>{});
+        return true;
+      }
     }
-    if constexpr (!WHOLE) fn(tl, tk, std::integral_constant<int, svr::FIT_ANY>{});
-    return !WHOLE;
+    if constexpr (L <= 512) fn(tl, tk, std::integral_constant<int, svr::FIT_ANY>{});
+    return L <= 512;
   };
 #define SV_TILE(L, V) \
   if (tile(std::integral_constant<int, L>{}, std::integral_constant<int, (V) / VE>{})) return true;
-  SV_TILE(1, 8) SV_TILE(2, 8) SV_TILE(4, 8) SV_TILE(8, 8) SV_TILE(8, 16)
+  SV_TILE(1, 8) SV_TILE(4, 8) SV_TILE(8, 8) SV_TILE(8, 16)
   SV_TILE(16, 16) SV_TILE(32, 16) SV_TILE(64, 16) SV_TILE(64, 24)
   SV_TILE(128, 16) SV_TILE(256, 16) SV_TILE(256, 24) SV_TILE(512, 16) SV_TILE(512, 24)
   SV_TILE(1024, 16)
@@ -188,7 +195,7 @@ int64_t grad_blocks(int dtype, int sum_dtype, int64_t rows, int64_t n) {
   int64_t blocks = 0;
   svm::with_types(dtype, sum_dtype, [&](auto t, auto u) {
     constexpr int VE = svm::chunk_values<decltype(t), decltype(u)>();
-    with_tile<VE>(n, [&](auto tl, auto tk, auto) {
+    with_tile<VE>(n, false, [&](auto tl, auto tk, auto) {
       constexpr int L = decltype(tl)::value, E = decltype(tk)::value * VE;
       constexpr int64_t R = grad_tpb(L, E, VE) / L;
       const int64_t all = (rows + R - 1) / R;
@@ -397,7 +404,7 @@ sv_status sv_rms_norm_backward(const void *dy, int64_t lddy, const void *h, int6
       float *part = dweight ? reinterpret_cast<float *>(workspace) : nullptr;
       const bool stream = rows * n * (int64_t)(sizeof(T) + (d ? 2 : 1) * sizeof(S)) > svm::LAST_LEVEL / 4 * 3;
       if (rows > 0)
-        with_tile<VE>(n, [&](auto tl, auto tk, auto tf) {
+        with_tile<VE>(n, stream, [&](auto tl, auto tk, auto tf) {
           constexpr int L = decltype(tl)::value, K = decltype(tk)::value, FIT = decltype(tf)::value;
           const auto rows_of = [&](auto sum, auto st) {
             k_rms_grad<T, S, decltype(sum)::value, decltype(st)::value, L, K, FIT>
@@ -408,11 +415,10 @@ sv_status sv_rms_norm_backward(const void *dy, int64_t lddy, const void *h, int6
             if (dsum) rows_of(std::true_type{}, st);
             else rows_of(std::false_type{}, st);
           };
-          // rows of whole chunks only: the others are bound by more than the read
           if constexpr (FIT == svr::FIT_CHUNKS) {
             if (stream) return launch(std::true_type{});
           }
-          launch(std::false_type{});
+          if constexpr (FIT != svr::FIT_CHUNKS || L > 512) launch(std::false_type{});
         });
       if (dweight) join_columns(part, rows > 0 ? blocks : 0, n, dweight, param_dtype, s);
       return;

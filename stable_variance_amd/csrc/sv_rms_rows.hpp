@@ -118,9 +118,9 @@ constexpr int tpb(int L) { return L <= 128 ? 256 : L; }
 // rows (256 MB in) 241, 236, 229; 32768 rows 443, 434, 398.
 // Bound by the read and the write: 16384 x 8192 bf16 with a residual to 8 bits
 // 147 us, 6.4 TB/s, 200000 x 128 bf16 17.6 us, 5.8 TB/s (a copy in torch runs
-// at 4.9-5.4).  Short of that, few rows: 5003 x 1531 f16 to 8 bits 9.8 us, 2.3 TB/s, where
-// every wave has one row, whose loads, sums and stores follow each other; one
-// row of 4096 takes 2.8 us.
+// at 4.9-5.4).  Short of that, few rows: 5003 x 1531 f16 to 8 bits 9.8 us, 2.3
+// TB/s, where every wave has one row, whose loads, sums and stores follow each
+// other; one row of 4096 takes 2.8 us.
 template <class T, class S, bool RES, bool Q, bool STREAM, int L, int K, int FIT>
 __global__ __launch_bounds__(tpb(L)) void k_rms_rows(const T *__restrict__ x, int64_t ldx, const S *__restrict__ res,
                                                      int64_t ldr, Rows a, T *__restrict__ y, int64_t ldy,
@@ -276,7 +276,7 @@ bool with_tile(int64_t n, Fn &&fn) {
   // Up to 64 values: 8 per thread, so that a row's lanes read whole cache
   // lines together; then 16 (half the cost per value of the cross-lane sums),
   // or 24 where that leaves fewer threads idle; 32 for the longest rows.
-  SV_TILE(1, 8) SV_TILE(2, 8) SV_TILE(4, 8) SV_TILE(8, 8) SV_TILE(8, 16)
+  SV_TILE(1, 8) SV_TILE(4, 8) SV_TILE(8, 8) SV_TILE(8, 16)
   if constexpr (MIN == 16) SV_TILE(16, 8)  // the shortest rows where a block takes 16 or 32 threads
   if constexpr (MIN == 32) SV_TILE(32, 8)
   SV_TILE(16, 16) SV_TILE(32, 16) SV_TILE(64, 16) SV_TILE(64, 24)
@@ -297,14 +297,17 @@ void forward(const void *x, int64_t ldx, const void *residual, int64_t ldr, int 
     constexpr int VE = svm::chunk_values<T, S>();
     const bool stream = a.rows * a.n * (int64_t)(sizeof(T) + (RES ? sizeof(S) : 0)) >= svm::LAST_LEVEL;
     const bool held = with_tile<VE, Q ? BLOCK / VE : 1>(a.n, [&](auto tl, auto tk, auto tf) {
-      constexpr int L = decltype(tl)::value, K = decltype(tk)::value, TPB = tpb(L), R = TPB / L, FIT = decltype(tf)::value;
+      constexpr int L = decltype(tl)::value, K = decltype(tk)::value, FIT = decltype(tf)::value, TPB = tpb(L);
+      constexpr int R = TPB / L;
       const int64_t blocks = (a.rows + R - 1) / R, most = 256 * (2048 / TPB);
+      const unsigned grid = (unsigned)(blocks < most ? blocks : most);
       const auto rows = [&](auto st) {
-        k_rms_rows<T, S, RES, Q, decltype(st)::value, L, K, FIT><<<(unsigned)(blocks < most ? blocks : most), TPB, 0, s>>>(
+        k_rms_rows<T, S, RES, Q, decltype(st)::value, L, K, FIT><<<grid, TPB, 0, s>>>(
             (const T *)x, ldx, (const S *)residual, ldr, a, (T *)y, ldy, (S *)sum, ldsum, o);
       };
-      // rows of whole chunks only: the others are bound by more than the read
-      if constexpr (FIT == svr::FIT_CHUNKS) {
+      // longer rows of whole chunks only, as the others are bound by more than
+      // the read and every kernel is there once more for it
+      if constexpr (FIT == svr::FIT_CHUNKS && L >= 128) {
         if (stream) return rows(std::true_type{});
       }
       rows(std::false_type{});

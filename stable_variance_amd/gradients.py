@@ -108,11 +108,12 @@ def clip_grad_norm(grads, max_norm: float, out=None):
     their ``grad_norm``: returns ``(out, norm)``, the norm that they had.
 
     ``out`` is a list of tensors of the same shapes and types (new ones by
-    default); ``out=grads`` scales in place.  What is written must not overlap
-    another tensor of either list (``SvError``, or ``ValueError`` where it is not
-    contiguous); an entry of ``out`` that is the entry of ``grads`` is in place.  The device is not waited for, so a
-    norm that is Inf or NaN raises nothing: with Inf every finite value becomes
-    0 and an Inf becomes NaN, with NaN all values do.
+    default); ``out=grads`` scales in place, as does an entry of ``out`` that
+    is the entry of ``grads``.  Otherwise what is written must not overlap any
+    tensor of either list: contiguous tensors that do are refused (``SvError``),
+    and so is one strided tensor twice (``ValueError``).  The device is not
+    waited for, so a norm that is Inf or NaN raises nothing: with Inf every
+    finite value becomes 0 and an Inf becomes NaN, with NaN all values do.
     """
     max_norm = float(max_norm)
     if forward_ad._current_level < 0:
