@@ -32,7 +32,8 @@ constexpr int64_t GRAD_RUN = 32;
 // chunks per thread: dy, h and (SUM) dsum are read once, one cross-thread sum
 // per row gives c.  The column sums of the rows a group passes stay in
 // registers; at the end the workgroup's groups are added up through LDS into
-// its row of `part`, [gridDim.x][n] (part == nullptr: not asked for).
+// its row of `part`, [gridDim.x][n], or, by a single workgroup, to dw (part ==
+// nullptr: not asked for).
 // STREAM: what is read is loaded non-temporal, which leaves the last-level
 // cache to dh and its reader.  Measured between kernels that write dsum and dy
 // (with 256 MB of other stores between) and one that reads dh, n = 4096 bf16,
@@ -45,7 +46,7 @@ template <class T, class S, bool SUM, bool STREAM, int L, int K, int FIT>
 __global__ __launch_bounds__(grad_tpb(L, K * svm::chunk_values<T, S>(), svm::chunk_values<T, S>())) void k_rms_grad(
     const T *__restrict__ dy, int64_t lddy, const S *__restrict__ h, int64_t ldh, const S *__restrict__ dsum,
     int64_t ldds, Rows a, S *__restrict__ dh, int64_t lddh, T *__restrict__ dx, int64_t lddx,
-    float *__restrict__ part) {
+    float *__restrict__ part, void *__restrict__ dw) {
   constexpr int VE = svm::chunk_values<T, S>(), E = K * VE, TPB = grad_tpb(L, E, VE), R = TPB / L;
   using TT = svr::RowTile<T, L, K, FIT, VE>;
   using TS = svr::RowTile<S, L, K, FIT, VE>;
@@ -148,7 +149,8 @@ __global__ __launch_bounds__(grad_tpb(L, K * svm::chunk_values<T, S>(), svm::chu
   for (int j = threadIdx.x; j < n; j += TPB) {
     Node t = sv::zero_node();
     for (int q = 0; q < R; ++q) svr::add_to(t, cols[q * (L * E) + j]);
-    out[j] = sv::root_value(t);
+    if (gridDim.x == 1) svr::store_as(dw, j, a.pt, sv::root_value(t));
+    else out[j] = sv::root_value(t);
   }
 }
 
@@ -409,7 +411,7 @@ sv_status sv_rms_norm_backward(const void *dy, int64_t lddy, const void *h, int6
           const auto rows_of = [&](auto sum, auto st) {
             k_rms_grad<T, S, decltype(sum)::value, decltype(st)::value, L, K, FIT>
                 <<<(unsigned)blocks, grad_tpb(L, K * VE, VE), 0, s>>>(g, lddy, x, ldh, d, lddsum, a, (S *)dh, lddh,
-                                                                      (T *)dx, lddx, part);
+                                                                      (T *)dx, lddx, part, dweight);
           };
           const auto launch = [&](auto st) {
             if (dsum) rows_of(std::true_type{}, st);
@@ -420,7 +422,7 @@ sv_status sv_rms_norm_backward(const void *dy, int64_t lddy, const void *h, int6
           }
           if constexpr (FIT != svr::FIT_CHUNKS || L > 512) launch(std::false_type{});
         });
-      if (dweight) join_columns(part, rows > 0 ? blocks : 0, n, dweight, param_dtype, s);
+      if (dweight && (rows == 0 || blocks > 1)) join_columns(part, rows > 0 ? blocks : 0, n, dweight, param_dtype, s);
       return;
     }
     Node *part = reinterpret_cast<Node *>(workspace);

@@ -2,8 +2,8 @@
 // for the calls of the root-mean-square norm and of the gradients' norm.
 //
 // Every function takes the arguments of the Python function of its name and
-// does what that does for ordinary ones: contiguous tensors on the current
-// device, nothing to record for autograd.  For anything else, and wherever the
+// does what that does for ordinary ones: tensors on the current device whose
+// values, or whose rows, lie in order in memory, nothing to record for autograd.  For anything else, and wherever the
 // library refuses the call, it returns None and has launched nothing; the
 // Python function then takes the general way, which converts or raises.  A
 // call of rms_norm costs the host 5 us here and 9 us there (its launch alone
@@ -32,15 +32,35 @@ int code_of(const at::Tensor &t) {
   }
 }
 
-// An ordinary tensor of one of the three types: no subclass, no wrapper, all
-// of its values in order in device memory.
-const at::Tensor *ordinary(PyObject *obj) {
+// An ordinary tensor of one of the three types: no subclass, no wrapper, in
+// device memory.
+const at::Tensor *strided(PyObject *obj) {
   if (!THPVariable_CheckExact(obj)) return nullptr;
   const at::Tensor &t = THPVariable_Unpack(obj);
-  if (t.layout() != at::kStrided || !t.is_cuda() || !t.has_storage() || code_of(t) < 0 || t.is_neg() ||
-      !t.is_contiguous())
-    return nullptr;
+  if (t.layout() != at::kStrided || !t.is_cuda() || !t.has_storage() || code_of(t) < 0 || t.is_neg()) return nullptr;
   return &t;
+}
+
+// All of its values in order, too.
+const at::Tensor *ordinary(PyObject *obj) {
+  const at::Tensor *t = strided(obj);
+  return t && t->is_contiguous() ? t : nullptr;
+}
+
+// The distance between the rows (of the last dimension) of a tensor that has
+// values, each row in order and all rows equally far apart; 0 for another.
+int64_t row_stride(const at::Tensor &t) {
+  const int64_t n = t.size(-1);
+  if (t.is_contiguous()) return n;
+  if (n > 1 && t.stride(-1) != 1) return 0;
+  int64_t ld = -1, next = 0;  // -1: one row so far
+  for (int64_t i = t.dim() - 2; i >= 0; --i) {
+    if (t.size(i) == 1) continue;
+    if (ld < 0) ld = t.stride(i);
+    else if (t.stride(i) != next) return 0;
+    next = t.stride(i) * t.size(i);
+  }
+  return ld < 0 ? n : ld >= n ? ld : 0;
 }
 
 bool records(const at::Tensor *t) { return t && t->requires_grad(); }
@@ -55,8 +75,8 @@ PyObject *rms(PyObject *, PyObject *const *args, Py_ssize_t count) {
   const long to = PyLong_AsLong(args[5]), block = PyLong_AsLong(args[6]);
   if (PyErr_Occurred()) return nullptr;
   const bool has_w = args[1] != Py_None, has_r = args[2] != Py_None;
-  const at::Tensor *x = ordinary(args[0]), *w = has_w ? ordinary(args[1]) : nullptr,
-                   *r = has_r ? ordinary(args[2]) : nullptr;
+  const at::Tensor *x = strided(args[0]), *w = has_w ? ordinary(args[1]) : nullptr,
+                   *r = has_r ? strided(args[2]) : nullptr;
   if (!x || (has_w && !w) || (has_r && !r) || x->dim() < 1 || x->numel() == 0) Py_RETURN_NONE;
   if (c10::GradMode::is_enabled() && (records(x) || records(w) || records(r))) Py_RETURN_NONE;
   const int64_t n = x->size(-1), rows = x->numel() / n;
@@ -66,6 +86,8 @@ PyObject *rms(PyObject *, PyObject *const *args, Py_ssize_t count) {
   if (w && (w->dim() != 1 || w->size(0) != n || w->device() != device)) Py_RETURN_NONE;
   if (r && (r->sizes() != x->sizes() || r->device() != device)) Py_RETURN_NONE;
   if ((wcode != code && wcode != SV_DTYPE_F32) || (rcode != code && rcode != SV_DTYPE_F32)) Py_RETURN_NONE;
+  const int64_t ldx = row_stride(*x), ldr = r ? row_stride(*r) : n;
+  if (!ldx || !ldr) Py_RETURN_NONE;
 
   const auto options = x->options().requires_grad(false);
   const at::Tensor y = at::empty(
@@ -83,9 +105,9 @@ PyObject *rms(PyObject *, PyObject *const *args, Py_ssize_t count) {
   const void *wp = w ? w->const_data_ptr() : nullptr, *rp = r ? r->const_data_ptr() : nullptr;
   void *stream = c10::hip::getCurrentHIPStream(device.index()).stream();
   const sv_status st =
-      to == 0 ? sv_rms_norm(x->const_data_ptr(), n, rp, n, code, rcode, rows, n, wp, wcode, eps, at_of(y), n, at_of(h),
-                            n, (float *)at_of(rstd), stream)
-              : sv_rms_norm_fp8(x->const_data_ptr(), n, rp, n, code, rcode, rows, n, wp, wcode, eps, (int)to, block,
+      to == 0 ? sv_rms_norm(x->const_data_ptr(), ldx, rp, ldr, code, rcode, rows, n, wp, wcode, eps, at_of(y), n,
+                            at_of(h), n, (float *)at_of(rstd), stream)
+              : sv_rms_norm_fp8(x->const_data_ptr(), ldx, rp, ldr, code, rcode, rows, n, wp, wcode, eps, (int)to, block,
                                 at_of(y), n, (float *)at_of(scale), at_of(h), n, (float *)at_of(rstd), stream);
   if (st != SV_OK) Py_RETURN_NONE;
   if (to == 0 && !r && !want_rstd) return THPVariable_Wrap(y);
@@ -106,8 +128,8 @@ PyObject *rms_backward(PyObject *, PyObject *const *args, Py_ssize_t count) {
   HANDLE_TH_ERRORS
   if (count != 8) return PyErr_Format(PyExc_TypeError, "rms_backward takes 8 arguments");
   const bool has_d = args[4] != Py_None;
-  const at::Tensor *dy = ordinary(args[0]), *h = ordinary(args[1]), *rstd = ordinary(args[2]), *w = ordinary(args[3]),
-                   *d = has_d ? ordinary(args[4]) : nullptr;
+  const at::Tensor *dy = strided(args[0]), *h = strided(args[1]), *rstd = ordinary(args[2]), *w = ordinary(args[3]),
+                   *d = has_d ? strided(args[4]) : nullptr;
   if (!dy || !h || !rstd || !w || (has_d && !d) || h->dim() < 1 || h->numel() == 0) Py_RETURN_NONE;
   const int64_t n = h->size(-1), rows = h->numel() / n;
   const int code = code_of(*dy), hcode = code_of(*h), wcode = code_of(*w);
@@ -120,6 +142,8 @@ PyObject *rms_backward(PyObject *, PyObject *const *args, Py_ssize_t count) {
       w->size(0) != n)
     Py_RETURN_NONE;
   if ((wcode != code && wcode != SV_DTYPE_F32) || (hcode != code && hcode != SV_DTYPE_F32)) Py_RETURN_NONE;
+  const int64_t lddy = row_stride(*dy), ldh = row_stride(*h), ldd = d ? row_stride(*d) : n;
+  if (!lddy || !ldh || !ldd) Py_RETURN_NONE;
 
   at::Tensor out[3], ws;
   const at::Tensor *like[3] = {h, dy, w};
@@ -136,8 +160,8 @@ PyObject *rms_backward(PyObject *, PyObject *const *args, Py_ssize_t count) {
     ws = at::empty({(int64_t)bytes}, h->options().requires_grad(false).dtype(at::kByte));
   }
   const sv_status st = sv_rms_norm_backward(
-      dy->const_data_ptr(), n, h->const_data_ptr(), n, d ? d->const_data_ptr() : nullptr, n, code, hcode, rows, n,
-      w->const_data_ptr(), wcode, (const float *)rstd->const_data_ptr(), p[0], n, p[1], n, p[2],
+      dy->const_data_ptr(), lddy, h->const_data_ptr(), ldh, d ? d->const_data_ptr() : nullptr, ldd, code, hcode, rows,
+      n, w->const_data_ptr(), wcode, (const float *)rstd->const_data_ptr(), p[0], n, p[1], n, p[2],
       ws.defined() ? ws.data_ptr() : nullptr, bytes, c10::hip::getCurrentHIPStream(device.index()).stream());
   if (st != SV_OK) Py_RETURN_NONE;
   PyObject *result = PyTuple_New(3);

@@ -237,8 +237,8 @@ _BLOCK = 128  # values that share a scale
 
 
 def _short(x, weight, eps, residual, want_rstd, out_code=0, block=0):
-    """The call for ordinary tensors (contiguous, on the current device, nothing
-    to record), None for others."""
+    """The call for ordinary tensors (rows in order in memory, on the current
+    device, nothing to record), None for others."""
     if forward_ad._current_level >= 0:
         return None
     return native().rms(x, weight, residual, eps, want_rstd, out_code, block)

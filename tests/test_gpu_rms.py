@@ -620,6 +620,17 @@ def test_both_ways_give_the_same(dev, monkeypatch):
                                       sv.rms_norm_fp8(x, w, 0.01, r, to, block, rstd)))
     from stable_variance_amd import native
 
+    # strided rows: a column range, two dimensions of rows, one row, one column
+    for dtype in TYPES:
+        wide = hidden(24, 51, dtype, 5)
+        for x in (wide[:, 3:43], wide.reshape(4, 6, 51)[..., :40], wide.reshape(2, 3, 4, 51)[:, :, :, 1:42],
+                  wide.reshape(4, 1, 6, 51)[..., 5:], wide[:1, 1:], wide[::2, :40], wide[:, 7:8], wide[2, 3:20],
+                  wide.reshape(4, 6, 51)[:, :1, 2:9]):
+            n = x.shape[-1]
+            for r in (None, x.contiguous(), hidden(24 * 51, 2, F32, 6).reshape(-1)[:x.numel()].reshape(x.shape), x):
+                w = weights(n, F32, 4)
+                calls.append((lambda x=x, w=w, r=r: sv.rms_norm(x, w, 0.01, r, True)))
+                calls.append((lambda x=x, w=w, r=r: sv.rms_norm_fp8(x, w, 0.01, r, E4M3, 128, True)))
     real, taken = native(), []
 
     class Counted:
@@ -659,6 +670,14 @@ def test_both_ways_back_give_the_same(dev, monkeypatch):
                 for d in (None, dsum):
                     for dw in (True, False):
                         calls.append((dy, h, rstd, w, d, dw))
+    for dtype, stream in PAIRS:
+        wide, rows = hidden(24, 51, stream, 5), hidden(24, 60, dtype, 6)
+        for a, b in ((wide[:, 3:43], rows[:, :40]), (wide.reshape(4, 6, 51)[..., :40], rows.reshape(4, 6, 60)[..., 20:]),
+                     (wide[:1, 1:], rows[:1, :50]), (wide[::2, :40], rows[1::2, 3:43]), (wide[2, 3:20], rows[3, 3:20]),
+                     (wide[:, 7:8], rows[:, 9:10])):
+            rstd = sv.rms_norm(a, return_rstd=True)[1]
+            for d in (None, a, a.contiguous()):
+                calls.append((b, a, rstd, weights(a.shape[-1], dtype, 3), d, True))
     for dy, h, rstd, w, d, dw in calls:
         out = layers._short_backward(dy, h, rstd, w, d, True, True, dw)
         assert out is not None
@@ -701,8 +720,10 @@ def test_the_short_way_leaves_the_others(dev):
     x, w, r = hidden(4, 8, BF16, 1), weights(8, F32, 1), hidden(4, 8, F32, 2)
     ok = (x, w, r, 1e-6, False, 0, 0)
     assert m.rms(*ok) is not None
+    square = hidden(8, 8, BF16, 4)
     half_view = torch.randn(4, 8, dtype=torch.complex64, device=dev).conj().imag
-    for i, bad in ((0, x.cpu()), (0, x.double()), (0, x[:, ::2]), (0, x.t()), (0, x[:0]), (0, x[:, :0]), (0, x[0, 0]),
+    for i, bad in ((0, x.cpu()), (0, x.double()), (0, x[:, ::2]), (0, square.t()), (0, square.as_strided((4, 8), (5, 1))),
+                   (0, square.reshape(2, 4, 8).transpose(0, 1)), (0, square[:1].expand(4, 8)), (0, x[:0]), (0, x[:, :0]), (0, x[0, 0]),
                    (0, 1.0), (0, None), (0, x.to_sparse()), (0, half_view), (0, torch._neg_view(x)),
                    (0, x.clone().requires_grad_()), (1, w.clone().requires_grad_()), (2, r.clone().requires_grad_()),
                    (1, w[:7]), (1, w[None]), (1, w.to(F16)), (1, w.cpu()), (1, w.double()), (1, [1.0] * 8),

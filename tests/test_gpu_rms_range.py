@@ -153,3 +153,23 @@ def test_column_join_in_batches_gives_the_same_bits(dev, dtype):
             finally:
                 sv.set_tuning("reset", 0)
             assert all(torch.equal(p, q) for p, q in zip(got, want)), (rows, n, items)
+
+
+@pytest.mark.parametrize("dtype,stream", PAIRS, ids=PAIR_IDS)
+def test_column_sums_of_one_workgroup(dev, dtype, stream):
+    # a batch that one workgroup holds writes the weight's gradient itself:
+    # the same sums as with a row of zeros far behind, which takes a second one
+    for n in (5, 64, 300, 1531, 4096, 8192, 16384):
+        for rows in (1, 2, 3):
+            w = weights(n, dtype, n)
+            h, dy = hidden(rows, n, stream, n), hidden(rows, n, dtype, n + 1)
+            rstd = sv.rms_norm(h, return_rstd=True)[1]
+            one = check_backward(h, dy, w, rstd=rstd)
+            more = torch.zeros(3000, n, dtype=dtype, device=dev)
+            more[:rows] = dy
+            wide = hidden(3000, n, stream, 3).clone()
+            wide[:rows] = h
+            long = torch.ones(3000, device=dev)
+            long[:rows] = rstd
+            check_backward(wide, more, w, rstd=long)
+            assert torch.equal(one[0], sv.rms_norm_backward(more, wide, long, w)[0][:rows])
