@@ -479,3 +479,55 @@ def test_the_short_way_leaves_the_others(dev):
         m.clip_grad_norm([a], "x", None)
     with pytest.raises(TypeError):
         m.clip_grad_norm([a], 1.0)
+
+
+def test_c_abi_without_tensors(dev):
+    import ctypes
+
+    L = sv.capi()
+    st = torch.cuda.current_stream().cuda_stream
+    ws = torch.full((256,), 7, dtype=torch.uint8, device=dev)
+    norm = torch.full((), 9.0, device=dev)
+    for sizes in ([], [0], [0, 0, 0]):
+        n = len(sizes)
+        p, s, t = (ctypes.c_void_p * n)(), (ctypes.c_int64 * n)(*sizes), (ctypes.c_int * n)()
+        args = (p, s, t) if n else (None, None, None)
+        norm.fill_(9.0)
+        assert L.sv_grad_norm(*args, n, norm.data_ptr(), ws.data_ptr(), 256, st) == 0
+        assert float(norm) == 0.0
+        norm.fill_(9.0)
+        assert L.sv_clip_grad_norm(args[0], args[0], *args[1:], n, 1.0, norm.data_ptr(), ws.data_ptr(), 256, st) == 0
+        assert float(norm) == 0.0
+
+
+def test_a_workspace_keeps_nothing(dev):
+    # one workspace for calls of different lists in turn, as two graphs would
+    # share it in stream order: what one call left does not reach the next
+    import ctypes
+
+    L = sv.capi()
+    st = torch.cuda.current_stream().cuda_stream
+    lists = [tensors([70000, 5, 300], TYPES, 1), tensors([3], [F32], 2), tensors([50] * 300, [BF16], 3)]
+    arrays, need = [], 0
+    for ts in lists:
+        n = len(ts)
+        a = ((ctypes.c_void_p * n)(*[t.data_ptr() for t in ts]), (ctypes.c_int64 * n)(*[t.numel() for t in ts]),
+             (ctypes.c_int * n)(*[{F32: 0, BF16: 1, F16: 2}[t.dtype] for t in ts]), n)
+        arrays.append(a)
+        need = max(need, L.sv_grad_norm_workspace_size(a[1], a[2], n))
+    ws = torch.randint(0, 256, (need,), dtype=torch.uint8, device=dev)
+    want = [sv.grad_norm(ts) for ts in lists]
+    for _ in range(2):
+        for a, w in zip(arrays, want):
+            norm = torch.empty((), device=dev)
+            assert L.sv_grad_norm(*a, norm.data_ptr(), ws.data_ptr(), need, st) == 0
+            assert torch.equal(norm, w)
+
+
+def test_many_tensors_of_one_value(dev):
+    flat = torch.arange(1, 5001, device=dev, dtype=F32)
+    ts = list(flat.split(1))
+    got = check_norm(ts)
+    assert abs(float(got) - math.sqrt(5000 * 5001 * 10001 / 6)) <= 2 * U * float(got)
+    check_clip(ts, 1.0, out=ts)
+    assert abs(float(flat.double().square().sum().sqrt()) - 1) < 1e-6
