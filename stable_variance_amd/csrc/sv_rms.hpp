@@ -280,7 +280,7 @@ inline sv_status check_forward(const char *who, const void *x, int64_t ldx, cons
   if (residual || sum) {
     if ((st = svr::check_matrix(who, "residual", residual, ldr, rows, n, se)) != SV_OK) return st;
     if ((st = svr::check_matrix(who, "sum", sum, ldsum, rows, n, se)) != SV_OK) return st;
-  } else if (sum_dtype != dtype) {
+  } else if (sum_dtype != dtype && rows > 0 && n > 0) {  // an empty residual may be NULL
     return svh::fail(SV_ERR_INVALID_ARGUMENT, "%s: sum_dtype %d without a residual must be dtype", who, sum_dtype);
   }
   if (weight && (st = svr::check_matrix(who, "weight", weight, n, 1, n, svr::dtype_bytes(param_dtype))) != SV_OK)

@@ -222,6 +222,27 @@ def test_empty(dev):
         assert q.shape == (0, 5) and scale.shape == (0, 1)
 
 
+@pytest.mark.parametrize("dtype,stream", STREAMS, ids=STREAM_IDS)
+def test_empty_batches_of_every_type(dev, dtype, stream):
+    for shape in ((0, 5), (0, 4096), (2, 0, 8), (3, 0), (0,), (0, 0)):
+        x = torch.empty(shape, dtype=dtype, device=dev)
+        r = None if stream is None else torch.empty(shape, dtype=stream, device=dev)
+        w = weights(shape[-1], F32, 1)
+        out = sv.rms_norm(x, w, residual=r, return_rstd=True)
+        assert out[0].shape == shape and out[0].dtype == dtype and out[-1].shape == shape[:-1]
+        assert r is None or (out[1].shape == shape and out[1].dtype == stream)
+        for block, blocks in ((128, -(-shape[-1] // 128)), (None, 1)):
+            q = sv.rms_norm_fp8(x, w, residual=r, block=block)
+            assert q[0].shape == shape and q[1].shape == shape[:-1] + (blocks,)
+        h = x if r is None else out[1]
+        dh, dw = sv.rms_norm_backward(out[0], h, out[-1], w, h)
+        assert dh.shape == shape and dh.dtype == h.dtype and torch.equal(dw, torch.zeros_like(w))
+        leaves = [t.clone().requires_grad_() for t in (x, w) + (() if r is None else (r,))]
+        y = sv.rms_norm(leaves[0], leaves[1], residual=None if r is None else leaves[2])
+        (y if r is None else y[0] + y[1]).sum().backward()
+        assert all(t.grad.shape == t.shape and (t.grad == 0).all() for t in leaves)
+
+
 def test_rows_far_apart(dev):
     ld = (1 << 30) + 8  # the third row starts beyond 2^31 values
     x = torch.empty(3, ld, dtype=BF16, device=dev)[:, :1000]

@@ -63,6 +63,7 @@ def test_forward_refusals(L):
         assert call(L, rows=1 << 20, res=P, sum=P, lds=1 << 40) == UNSUPPORTED
         assert call(L, rows=(1 << 36) + 1, n=0) == UNSUPPORTED
         assert call(L, rows=0, x=None) == 0  # no rows: nothing to do
+        assert call(L, rows=0, x=None, dtype=1, sd=0) == 0  # an empty residual may be NULL
 
 
 def backward(L, dy=P, lddy=8, h=P, ldh=8, ds=None, ldds=8, dtype=0, sd=0, rows=4, n=8, w=None, pt=0, rstd=P, dh=P,
