@@ -122,9 +122,9 @@ __device__ __forceinline__ double square(float v) { return (double)v * (double)v
 // Inf: a maximum over them keeps a NaN, as float's own maximum does not.
 __device__ __forceinline__ unsigned abs_bits(float v) { return __builtin_bit_cast(unsigned, v) & 0x7fffffffu; }
 
-// VE values of type T from p on as float32, of which `count` are there
-// (the others are 0 and not read).
-template <class T, int VE>
+// VE values of type T from p on as float32, of which `count` are there (the
+// others are 0 and not read).  Without TAIL all are there or none.
+template <class T, int VE, bool TAIL = true>
 __device__ __forceinline__ void get(const T *p, int count, float (&f)[VE]) {
   typedef T Vec __attribute__((ext_vector_type(VE)));
   if (count >= VE) {
@@ -134,7 +134,7 @@ __device__ __forceinline__ void get(const T *p, int count, float (&f)[VE]) {
     for (int i = 0; i < VE; ++i) f[i] = svr::to_f<T>(v[i]);
   } else {
 #pragma unroll
-    for (int i = 0; i < VE; ++i) f[i] = i < count ? svr::to_f<T>(p[i]) : 0.0f;
+    for (int i = 0; i < VE; ++i) f[i] = TAIL && i < count ? svr::to_f<T>(p[i]) : 0.0f;
   }
 }
 
@@ -154,19 +154,17 @@ __device__ __forceinline__ void put(T *p, int count, const float (&f)[VE]) {
   }
 }
 
-// VE values of a parameter vector whose type is a launch argument, `count` of
-// them there; 1 for p == nullptr.
-template <int VE>
+// VE values of a parameter vector beside rows of T, whose type (T or float32)
+// is a launch argument, `count` of them there; 1 for p == nullptr.
+template <class T, int VE, bool TAIL = true>
 __device__ __forceinline__ void get_weight(const void *p, int dtype, int64_t at, int count, float (&f)[VE]) {
   if (!p) {
 #pragma unroll
     for (int i = 0; i < VE; ++i) f[i] = 1.0f;
-  } else if (dtype == SV_DTYPE_BF16) {
-    get<bf16, VE>(reinterpret_cast<const bf16 *>(p) + at, count, f);
-  } else if (dtype == SV_DTYPE_F16) {
-    get<f16, VE>(reinterpret_cast<const f16 *>(p) + at, count, f);
+  } else if (sizeof(T) == 2 && dtype != SV_DTYPE_F32) {
+    get<T, VE, TAIL>(reinterpret_cast<const T *>(p) + at, count, f);
   } else {
-    get<float, VE>(reinterpret_cast<const float *>(p) + at, count, f);
+    get<float, VE, TAIL>(reinterpret_cast<const float *>(p) + at, count, f);
   }
 }
 
@@ -193,13 +191,13 @@ __device__ __forceinline__ unsigned fp8_pair(float a, float b, bool e5m2) {
 }
 
 // `count` of VE values f * inv (inv: the scale's reciprocal) to p.
-template <int VE>
+template <int VE, bool TAIL = true>
 __device__ __forceinline__ void put_fp8(uint8_t *p, int count, const float (&f)[VE], float inv, bool e5m2) {
   unsigned w[VE / 4];
 #pragma unroll
   for (int i = 0; i < VE; i += 4)
     w[i / 4] = fp8_pair(f[i] * inv, f[i + 1] * inv, e5m2) | fp8_pair(f[i + 2] * inv, f[i + 3] * inv, e5m2) << 16;
-  if (count >= VE) {
+  if (!TAIL || count >= VE) {
     __builtin_memcpy(p, w, VE);
   } else {
 #pragma unroll

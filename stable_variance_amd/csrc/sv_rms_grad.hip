@@ -83,7 +83,7 @@ __global__ __launch_bounds__(grad_tpb(L, K * svm::chunk_values<T, S>(), svm::chu
 #pragma unroll
   for (int k = 0; k < K; ++k) {  // in flight beside the first row
     const int e = TT::first(l0, k), left = n - e;
-    svm::get_weight<VE>(a.w, a.pt, e, left < 0 ? 0 : left, wv[FEW ? 0 : k]);
+    svm::get_weight<T, VE, FIT != svr::FIT_CHUNKS>(a.w, a.pt, e, left < 0 ? 0 : left, wv[FEW ? 0 : k]);
     if constexpr (FEW) {
 #pragma unroll
       for (int i = 0; i < VE; ++i) wlds[e + i] = wv[0][i];
@@ -226,7 +226,7 @@ __global__ __launch_bounds__(ROW_THREADS) void k_rms_dh_any(const T *dy, int64_t
       float w[VE];
       svm::get<S, VE>(h + r * ldh + e, count, xh);
       svm::get<T, VE>(dy + r * lddy + e, count, g);
-      svm::get_weight<VE>(a.w, a.pt, e, count, w);
+      svm::get_weight<T, VE>(a.w, a.pt, e, count, w);
 #pragma unroll
       for (int i = 0; i < VE; ++i) {
         xh[i] = xh[i] * rs;

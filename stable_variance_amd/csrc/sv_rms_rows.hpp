@@ -45,7 +45,7 @@ __global__ __launch_bounds__(ROW_THREADS) void k_rms_any(const T *x, int64_t ldx
       float w[VE];
       if constexpr (RES) svm::get<S, VE>(h + r * ldh + e, count, f);
       else svm::get<T, VE>(xr + e, count, f);
-      svm::get_weight<VE>(a.w, a.pt, e, count, w);
+      svm::get_weight<T, VE>(a.w, a.pt, e, count, w);
 #pragma unroll
       for (int i = 0; i < VE; ++i) f[i] = (f[i] * rs) * w[i];
     };
@@ -126,7 +126,7 @@ __global__ __launch_bounds__(tpb(L)) void k_rms_rows(const T *__restrict__ x, in
                                                      int64_t ldr, Rows a, T *__restrict__ y, int64_t ldy,
                                                      S *__restrict__ h, int64_t ldh, Out8 o) {
   constexpr int VE = svm::chunk_values<T, S>(), E = K * VE, TPB = tpb(L), R = TPB / L;
-  constexpr bool HOLD = E <= 24;
+  constexpr bool HOLD = E <= 24, TAIL = FIT != svr::FIT_CHUNKS;
   using TX = svr::RowTile<T, L, K, FIT, VE>;
   using TS = svr::RowTile<S, L, K, FIT, VE>;
   __shared__ double lds_sum[2][TPB / 64];
@@ -137,7 +137,7 @@ __global__ __launch_bounds__(tpb(L)) void k_rms_rows(const T *__restrict__ x, in
   float wv[HOLD ? K : 1][VE];
   const auto weight = [&](int l, int k, float(&w)[VE]) {
     const int e = TX::first(l, k), left = n - e;
-    svm::get_weight<VE>(a.w, a.pt, e, left < 0 ? 0 : left, w);
+    svm::get_weight<T, VE, TAIL>(a.w, a.pt, e, left < 0 ? 0 : left, w);
   };
   const int64_t step = (int64_t)gridDim.x * R;
   typename TX::Vec rx[K];
@@ -219,7 +219,7 @@ __global__ __launch_bounds__(tpb(L)) void k_rms_rows(const T *__restrict__ x, in
         float v[VE];
 #pragma unroll
         for (int i = 0; i < VE; ++i) v[i] = f[k * VE + i];
-        if (own && left > 0) svm::put_fp8<VE>(o.q + r * o.ldq + e, left, v, inv, o.e5m2);
+        if (own && left > 0) svm::put_fp8<VE, TAIL>(o.q + r * o.ldq + e, left, v, inv, o.e5m2);
       };
 #pragma unroll
       for (int k = 0; k < K; ++k) scale_chunk(k);
