@@ -539,6 +539,14 @@ def test_autograd(dev):
             for i, (leaf, want) in enumerate(zip(leaves, (dh.to(dtype), dw, dh))):
                 assert (leaf.grad is None) == (not mask >> i & 1)
                 assert leaf.grad is None or torch.equal(leaf.grad, want), (mask, i)
+        # both inputs have a gradient of their own, which may be changed in place
+        a, b = (t.clone().requires_grad_() for t in (x, r))
+        torch.autograd.backward(sv.rms_norm(a, w, residual=b), (dy, dsum))
+        assert a.grad.data_ptr() != b.grad.data_ptr()
+        sv.clip_grad_norm([a.grad, b.grad], 1e-3, out=[a.grad, b.grad])
+        a, b = (t.clone().requires_grad_() for t in (x, r))
+        sv.rms_norm(a, w, residual=b)[1].backward(dsum)
+        assert len({a.grad.data_ptr(), b.grad.data_ptr(), dsum.data_ptr()}) == 3
         # one of the two results alone
         a, b = (t.clone().requires_grad_() for t in (x, r))
         sv.rms_norm(a, w, residual=b)[0].backward(dy)

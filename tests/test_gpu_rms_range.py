@@ -173,3 +173,29 @@ def test_column_sums_of_one_workgroup(dev, dtype, stream):
             long[:rows] = rstd
             check_backward(wide, more, w, rstd=long)
             assert torch.equal(one[0], sv.rms_norm_backward(more, wide, long, w)[0][:rows])
+
+
+def test_more_than_2_31_values(dev):
+    rows, n = 525_000, 4096
+    assert rows * n > 1 << 31
+    x = torch.empty(rows, n, dtype=BF16, device=dev)
+    for i in range(0, rows, 75_000):
+        x[i:i + 75_000] = hidden(75_000, n, BF16, i)
+    w = weights(n, F32, 1)
+    y, h, rstd = sv.rms_norm(x, w, residual=x, return_rstd=True)
+    q, scale, h8 = sv.rms_norm_fp8(x, w, residual=x)
+    dh, dw = sv.rms_norm_backward(x, h, rstd, w, y)
+    for k in (0, 1, 262_144, 524_287, 524_288, rows - 2, rows - 1):
+        one = check_forward(x[k:k + 1], w, residual=x[k:k + 1])
+        assert all(torch.equal(p[k:k + 1], v) for p, v in zip((y, h, rstd), one)), k
+        one8 = check_fp8(x[k:k + 1], w, E4M3, 128, residual=x[k:k + 1])
+        assert all(same(p[k:k + 1], v) for p, v in zip((q, scale, h8), one8)), k
+        back = check_backward(h[k:k + 1], x[k:k + 1], w, y[k:k + 1], rstd=rstd[k:k + 1])
+        assert torch.equal(dh[k:k + 1], back[0]), k
+    want, size = torch.zeros(n, dtype=torch.float64, device=dev), torch.zeros(n, dtype=torch.float64, device=dev)
+    for i in range(0, rows, 75_000):
+        t = x[i:i + 75_000].double() * (h[i:i + 75_000].double() * rstd[i:i + 75_000].double()[:, None])
+        want += t.sum(0)
+        size += t.abs().sum(0)
+    # two roundings a term, runs of at most 48, joined with compensation
+    assert ((dw.double() - want).abs() <= 3 * 2.0 ** -24 * want.abs() + 52 * 2.0 ** -24 * size).all()

@@ -417,3 +417,17 @@ def test_dense_tensors():
     for bad in (t[:, 1], t[..., ::2], t[..., :3], torch.zeros(1).expand(4), torch.zeros(3, 1).expand(3, 4),
                 torch.zeros(20).as_strided((4, 4), (1, 1)), torch.zeros(20).as_strided((4, 4), (4, 2))):
         assert not gradients._dense(bad)
+
+
+def test_the_native_module_leaves_host_tensors():
+    m = sv.native()
+    x, w, s = torch.zeros(3, 4), torch.ones(4), torch.ones(3)
+    assert m.rms(x, w, None, 1e-6, False, 0, 0) is None and m.rms(x, w, x, 1e-6, True, 3, 128) is None
+    assert m.rms(None, None, None, 1e-6, False, 0, 0) is None and m.rms([1.0], w, None, 1e-6, False, 0, 0) is None
+    assert m.rms_backward(x, x, s, w, None, True, False, True) is None
+    for bad in ([x], [], None, x, (x, w), [None]):
+        assert m.grad_norm(bad) is None and m.clip_grad_norm(bad, 1.0, None) is None
+    for call in (lambda: m.rms(x, w), lambda: m.rms(x, w, None, "eps", False, 0, 0), lambda: m.rms_backward(x),
+                 lambda: m.clip_grad_norm([x], "most", None), lambda: m.clip_grad_norm([x])):
+        with pytest.raises(TypeError):
+            call()
