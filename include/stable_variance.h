@@ -559,12 +559,13 @@ sv_status sv_grad_norm(const void *const *tensors, const int64_t *sizes, const i
  * The same norm N (before its rounding), and every value scaled by
  *   k = min(1, max_norm / (N + 1e-6))        rounded to float32 (subnormal
  *                                            below 2^-126)
- * out = g * k, a float32 product rounded to the tensor's type.  With N = Inf k
- * is 0 (an Inf itself becomes NaN); with N = NaN every value becomes NaN.
+ * out = g * k, a float32 product rounded to the tensor's type.  With max_norm =
+ * Inf k is 1, else with N = Inf k is 0 (an Inf itself becomes NaN); with N = NaN
+ * every value becomes NaN, whatever max_norm is.
  *   out        host array of device addresses; out[i] may be tensors[i] (in
  *              place), else what is written must not overlap what is read or
  *              written for any tensor (SV_ERR_INVALID_ARGUMENT)
- *   max_norm   >= 0 (Inf: nothing is scaled)
+ *   max_norm   >= 0 (Inf: no limit, nothing is scaled)
  * The other arguments and the workspace as for sv_grad_norm.
  */
 sv_status sv_clip_grad_norm(const void *const *tensors, void *const *out, const int64_t *sizes, const int *dtypes,

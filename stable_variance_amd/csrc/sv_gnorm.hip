@@ -7,7 +7,8 @@
 // Squares and sums are held in double: the square of a float32 is exact
 // there, so no gradient is too large or too small for the sum, and N is good
 // to about 2^-45 before it is rounded to float32.  An Inf among the values
-// gives N = Inf and k = 0, a NaN gives NaN for both.
+// gives N = Inf and k = 0, a NaN gives NaN for both.  Without a limit (max_norm
+// = Inf) k is 1 for every N but NaN: Inf / Inf would make it NaN.
 //
 // The tensors' addresses and sizes travel in the launch's arguments, up to
 // TABLE tensors a launch, so that nothing is copied to the device.  Every
@@ -152,7 +153,7 @@ __global__ __launch_bounds__(JOIN_THREADS) void k_gnorm_join(const double *part,
   if (threadIdx.x == 0) {
     *norm = (float)v;
     if (factor) {
-      const double k = max_norm / (v + 1e-6);
+      const double k = __builtin_isinf(max_norm) && v == v ? 1.0 : max_norm / (v + 1e-6);
       *factor = k >= 1.0 ? 1.0f : (float)k;  // a NaN stays
     }
   }

@@ -114,6 +114,7 @@ def clip_grad_norm(grads, max_norm: float, out=None):
     and so is one strided tensor twice (``ValueError``).  The device is not
     waited for, so a norm that is Inf or NaN raises nothing: with Inf every
     finite value becomes 0 and an Inf becomes NaN, with NaN all values do.
+    ``max_norm=inf`` is no limit: nothing is scaled, unless the norm is NaN.
     """
     max_norm = float(max_norm)
     if forward_ad._current_level < 0:
