@@ -187,7 +187,10 @@ struct List {
 };
 
 // false: not a list or tuple of ordinary tensors on the current device.
-bool list_of(PyObject *obj, List &l) {
+// `written`: they get values.  A tensor that shares its memory until it is
+// written (torch's copy-on-write) then gets its own here, so the list that is
+// written comes before the one that is read.
+bool list_of(PyObject *obj, List &l, bool written = false) {
   if (!PyList_CheckExact(obj) && !PyTuple_CheckExact(obj)) return false;
   const Py_ssize_t count = PySequence_Fast_GET_SIZE(obj);
   if (!count) return false;
@@ -203,7 +206,7 @@ bool list_of(PyObject *obj, List &l) {
     if (i == 0) device = c10::hip::current_device();  // not before there is a tensor on a device
     if (t->device().index() != device) return false;
     l.t.push_back(t);
-    l.p.push_back(const_cast<void *>(t->const_data_ptr()));
+    l.p.push_back(written ? t->data_ptr() : const_cast<void *>(t->const_data_ptr()));
     l.n.push_back(t->numel());
     l.type.push_back(code_of(*t));
   }
@@ -244,18 +247,18 @@ PyObject *clip_grad_norm(PyObject *, PyObject *const *args, Py_ssize_t count) {
   if (count != 3) return PyErr_Format(PyExc_TypeError, "clip_grad_norm takes 3 arguments");
   const double max_norm = PyFloat_AsDouble(args[1]);
   if (PyErr_Occurred()) return nullptr;
-  List l;
-  if (!list_of(args[0], l)) Py_RETURN_NONE;
+  List l, given;
+  const bool has_out = args[2] != Py_None;
+  if ((has_out && !list_of(args[2], given, true)) || !list_of(args[0], l)) Py_RETURN_NONE;
   std::vector<at::Tensor> made;
   std::vector<void *> p;
-  List given;
-  if (args[2] == Py_None) {
+  if (!has_out) {
     for (const at::Tensor *t : l.t) {
       made.push_back(at::empty(t->sizes(), t->options().requires_grad(false)));
       p.push_back(made.back().data_ptr());
     }
   } else {
-    if (!list_of(args[2], given) || given.t.size() != l.t.size()) Py_RETURN_NONE;
+    if (given.t.size() != l.t.size()) Py_RETURN_NONE;
     for (size_t i = 0; i < l.t.size(); ++i) {
       if (given.t[i]->sizes() != l.t[i]->sizes() || given.type[i] != l.type[i] ||
           (c10::GradMode::is_enabled() && given.t[i]->requires_grad()))
@@ -268,7 +271,7 @@ PyObject *clip_grad_norm(PyObject *, PyObject *const *args, Py_ssize_t count) {
   for (const at::Tensor *t : given.t)
     if (!t->is_inference()) t->unsafeGetTensorImpl()->bump_version();
   PyObject *outs;
-  if (given.t.empty()) {
+  if (!has_out) {
     outs = PyList_New((Py_ssize_t)made.size());
     if (!outs) return nullptr;
     for (size_t i = 0; i < made.size(); ++i) PyList_SET_ITEM(outs, (Py_ssize_t)i, THPVariable_Wrap(made[i]));

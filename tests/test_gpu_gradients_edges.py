@@ -1,4 +1,5 @@
-"""Clipping where its limit or the norm is no number."""
+"""Clipping where its limit or the norm is no number, and of tensors that share
+memory until one of them is written."""
 import pytest
 import torch
 
@@ -41,3 +42,20 @@ def test_no_limit_above_float32(dev, way):
     many = torch.full((10000,), 3e38, device=dev)  # the norm is beyond float32, and a number
     out, norm = sv.clip_grad_norm([many], INF)
     assert float(norm) == INF and torch.equal(out[0], many)
+
+
+def test_shared_until_written(dev, way):
+    # copy-on-write: a tensor and its lazy clone, one memory as long as they are read
+    for dtype in TYPES:
+        first = tensors([3000], [dtype], 1)[0]
+        kept = first.clone()
+        want = sv.clip_grad_norm([kept], 0.5)[0][0]
+        lazy = torch._lazy_clone(first)
+        got, _ = sv.clip_grad_norm([lazy], 0.5, out=[lazy])  # in place
+        assert got[0] is lazy and torch.equal(lazy, want) and torch.equal(first, kept)
+        lazy = torch._lazy_clone(first)
+        sv.clip_grad_norm([first], 0.5, out=[lazy])  # from the other
+        assert torch.equal(lazy, want) and torch.equal(first, kept)
+        lazy = torch._lazy_clone(first)
+        sv.clip_grad_norm([lazy], 0.5, out=[first])
+        assert torch.equal(first, want) and torch.equal(lazy, kept)
