@@ -3,11 +3,12 @@
 //
 // Every function takes the arguments of the Python function of its name and
 // does what that does for ordinary ones: tensors on the current device whose
-// values, or whose rows, lie in order in memory, nothing to record for autograd.  For anything else, and wherever the
-// library refuses the call, it returns None and has launched nothing; the
-// Python function then takes the general way, which converts or raises.  A
-// call of rms_norm costs the host 5 us here and 9 us there (its launch alone
-// 3), a grad_norm over 37 tensors 9 and 28.
+// values, or whose rows, lie in order in memory, nothing to record for
+// autograd.  For anything else, and wherever the library refuses the call, it
+// returns None and has launched nothing; the Python function then takes the
+// general way, which converts or raises.  A failed launch raises here: some of
+// the call may have run.  A call of rms_norm costs the host 5 us here and 9 us
+// there (its launch alone 3), a grad_norm over 37 tensors 9 and 28.
 #include <Python.h>
 
 #include <ATen/ATen.h>
@@ -65,6 +66,17 @@ int64_t row_stride(const at::Tensor &t) {
 
 bool records(const at::Tensor *t) { return t && t->requires_grad(); }
 
+// What a call returns for a status that is not SV_OK: None where the library
+// refused it, the binding's exception where a launch failed.
+PyObject *not_done(sv_status st) {
+  if (st != SV_ERR_HIP) Py_RETURN_NONE;
+  PyObject *package = PyImport_ImportModule("stable_variance_amd");
+  if (!package) return nullptr;
+  PyObject *none = PyObject_CallMethod(package, "_check", "i", (int)st);  // raises
+  Py_DECREF(package);
+  return none;
+}
+
 // rms(x, weight, residual, eps, rstd, out_dtype, block): rms_norm for out_dtype
 // 0, else rms_norm_fp8 with the type code and the block (0: whole rows).
 PyObject *rms(PyObject *, PyObject *const *args, Py_ssize_t count) {
@@ -109,7 +121,7 @@ PyObject *rms(PyObject *, PyObject *const *args, Py_ssize_t count) {
                             at_of(h), n, (float *)at_of(rstd), stream)
               : sv_rms_norm_fp8(x->const_data_ptr(), ldx, rp, ldr, code, rcode, rows, n, wp, wcode, eps, (int)to, block,
                                 at_of(y), n, (float *)at_of(scale), at_of(h), n, (float *)at_of(rstd), stream);
-  if (st != SV_OK) Py_RETURN_NONE;
+  if (st != SV_OK) return not_done(st);
   if (to == 0 && !r && !want_rstd) return THPVariable_Wrap(y);
   PyObject *out = PyTuple_New(1 + (to != 0) + has_r + want_rstd);
   if (!out) return nullptr;
@@ -163,7 +175,7 @@ PyObject *rms_backward(PyObject *, PyObject *const *args, Py_ssize_t count) {
       dy->const_data_ptr(), lddy, h->const_data_ptr(), ldh, d ? d->const_data_ptr() : nullptr, ldd, code, hcode, rows,
       n, w->const_data_ptr(), wcode, (const float *)rstd->const_data_ptr(), p[0], n, p[1], n, p[2],
       ws.defined() ? ws.data_ptr() : nullptr, bytes, c10::hip::getCurrentHIPStream(device.index()).stream());
-  if (st != SV_OK) Py_RETURN_NONE;
+  if (st != SV_OK) return not_done(st);
   PyObject *result = PyTuple_New(3);
   if (!result) return nullptr;
   for (int i = 0; i < 3; ++i) {
@@ -213,30 +225,28 @@ bool list_of(PyObject *obj, List &l, bool written = false) {
   return true;
 }
 
-// The norm of `l` and, with `out`, the scaled tensors; undefined where the
-// library refuses.
-at::Tensor norm_of(const List &l, void *const *out, double max_norm) {
+// The norm of `l` and, with `out`, the scaled tensors; the library's status.
+sv_status norm_of(const List &l, void *const *out, double max_norm, at::Tensor &norm) {
   const int64_t count = (int64_t)l.t.size();
   const size_t bytes = sv_grad_norm_workspace_size(l.n.data(), l.type.data(), count);
-  if (bytes == (size_t)-1) return {};
+  if (bytes == (size_t)-1) return SV_ERR_UNSUPPORTED;
   const auto options = at::TensorOptions().device(l.t[0]->device());
-  const at::Tensor norm = at::empty({}, options.dtype(at::kFloat));
+  norm = at::empty({}, options.dtype(at::kFloat));
   const at::Tensor ws = at::empty({(int64_t)bytes}, options.dtype(at::kByte));
   void *stream = c10::hip::getCurrentHIPStream(l.t[0]->device().index()).stream();
-  const sv_status st =
-      out ? sv_clip_grad_norm(l.p.data(), out, l.n.data(), l.type.data(), count, max_norm, (float *)norm.data_ptr(),
-                              ws.data_ptr(), bytes, stream)
-          : sv_grad_norm(l.p.data(), l.n.data(), l.type.data(), count, (float *)norm.data_ptr(), ws.data_ptr(), bytes,
-                         stream);
-  return st == SV_OK ? norm : at::Tensor();
+  return out ? sv_clip_grad_norm(l.p.data(), out, l.n.data(), l.type.data(), count, max_norm, (float *)norm.data_ptr(),
+                                 ws.data_ptr(), bytes, stream)
+             : sv_grad_norm(l.p.data(), l.n.data(), l.type.data(), count, (float *)norm.data_ptr(), ws.data_ptr(),
+                            bytes, stream);
 }
 
 PyObject *grad_norm(PyObject *, PyObject *grads) {
   HANDLE_TH_ERRORS
   List l;
   if (!list_of(grads, l)) Py_RETURN_NONE;
-  const at::Tensor norm = norm_of(l, nullptr, 0.0);
-  if (!norm.defined()) Py_RETURN_NONE;
+  at::Tensor norm;
+  const sv_status st = norm_of(l, nullptr, 0.0, norm);
+  if (st != SV_OK) return not_done(st);
   return THPVariable_Wrap(norm);
   END_HANDLE_TH_ERRORS
 }
@@ -266,8 +276,9 @@ PyObject *clip_grad_norm(PyObject *, PyObject *const *args, Py_ssize_t count) {
     }
     p = given.p;
   }
-  const at::Tensor norm = norm_of(l, p.data(), max_norm);
-  if (!norm.defined()) Py_RETURN_NONE;
+  at::Tensor norm;
+  const sv_status st = norm_of(l, p.data(), max_norm, norm);
+  if (st != SV_OK) return not_done(st);
   for (const at::Tensor *t : given.t)
     if (!t->is_inference()) t->unsafeGetTensorImpl()->bump_version();
   PyObject *outs;
