@@ -3,10 +3,13 @@
  * before it): each is counted, launches nothing and returns stand_in_status.
  * Calls that are made through the library's own handle are not met.
  */
-int stand_in_status, stand_in_calls;
+int PyGILState_Check(void);
+
+int stand_in_status, stand_in_calls, stand_in_with_gil;
 
 static int taken(void) {
   ++stand_in_calls;
+  stand_in_with_gil += PyGILState_Check();
   return stand_in_status;
 }
 

@@ -1,5 +1,5 @@
 """The module that takes ordinary tensors to the library: what it does when a
-launch fails.
+launch fails, and whether other threads run meanwhile.
 
 A process of its own loads a stand-in for the library's calls before the
 module (tests/library_stand_in.c).  The stand-in launches nothing; the Python
@@ -45,6 +45,17 @@ assert (x == 1).all() and x._version == version
 print("done")
 """
 
+THREADS = HEAD + r"""
+number("stand_in_status").value = 1  # refused: the general way makes the call
+for call in calls:
+    call()
+torch.cuda.synchronize()
+assert number("stand_in_calls").value == len(calls)
+assert number("stand_in_with_gil").value == 0, number("stand_in_with_gil").value
+print("done")
+"""
+
+
 @pytest.fixture(scope="module")
 def stand_in(tmp_path_factory):
     if not torch.cuda.is_available():
@@ -71,3 +82,9 @@ def run(program, so):
 def test_a_call_whose_launch_failed_is_not_made_again(stand_in):
     # some of it may have run: in place, a second one would scale twice
     run(FAILED, stand_in)
+
+
+def test_other_threads_run_beside_the_library(stand_in):
+    # a launch waits when the queue is full; a thread that the queue waits for
+    # needs the interpreter's lock
+    run(THREADS, stand_in)
