@@ -2,6 +2,7 @@
 that passes torch's tensors to it, with g++ (both in-tree, no JIT cache)."""
 from __future__ import annotations
 
+import importlib.util
 import os
 import subprocess
 
@@ -57,53 +58,77 @@ def module_commands(obj: str, out: str):
     return [*cxx, "-c", MODULE_SRC, "-o", obj], link
 
 
+def _start(cmd):
+    try:
+        return cmd, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.PIPE, text=True)
+    except OSError as e:  # no such compiler
+        return cmd, e
+
+
+def _failure(cmd, started, verbose: bool) -> str:
+    """Waits for a command: what it said if it failed, else nothing."""
+    if isinstance(started, Exception):
+        return f"{' '.join(cmd)}\n{started}\n"
+    out, err = started.communicate()
+    if started.returncode != 0:
+        return " ".join(cmd) + "\n" + out + err
+    if verbose:
+        print(" ".join(cmd))
+    return ""
+
+
+def has_torch() -> bool:
+    """Whether torch is installed here: the module needs it, the library does not."""
+    return importlib.util.find_spec("torch") is not None
+
+
 def build(verbose: bool = False) -> str:
-    """Compile the sources (in parallel) and link the library and the module; returns the library's path."""
+    """Compile the sources (in parallel) and link the library and, where torch
+    is installed, the module; returns the library's path.  The library needs
+    hipcc alone and is in place before a failure of the module is raised."""
     os.makedirs(OUT_DIR, exist_ok=True)
-    flags = [f for f in HIPCC_FLAGS if f != "-shared"]
     module_obj, module_tmp = os.path.join(OUT_DIR, "sv_torch.o"), MODULE + ".tmp"
-    compile_module, link_module = module_commands(module_obj, module_tmp)
-    objs = []
-    procs = [(compile_module, subprocess.Popen(compile_module, stdout=subprocess.PIPE, stderr=subprocess.PIPE,
-                                               text=True))]
+    module, link_module = None, None
+    if has_torch():
+        try:
+            compile_module, link_module = module_commands(module_obj, module_tmp)
+            module = _start(compile_module)
+        except ImportError as e:
+            module = ["import torch"], e
+    flags = [f for f in HIPCC_FLAGS if f != "-shared"]
+    objs, started = [], []
     for src in SRCS:
         obj = os.path.join(OUT_DIR, os.path.splitext(os.path.basename(src))[0] + ".o")
-        cmd = [hipcc(), *flags, "-c", src, "-o", obj]
-        procs.append((cmd, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.PIPE, text=True)))
+        started.append(_start([hipcc(), *flags, "-c", src, "-o", obj]))
         objs.append(obj)
-    errors = []
-    for cmd, pr in procs:
-        out, err = pr.communicate()
-        if pr.returncode != 0:
-            errors.append(" ".join(cmd) + "\n" + out + err)
-        elif verbose:
-            print(" ".join(cmd))
+    errors = [e for e in [_failure(*s, verbose) for s in started] if e]
+    module_error = _failure(*module, verbose) if module else ""
     if errors:
         raise RuntimeError("hipcc failed:\n" + "\n".join(errors))
     tmp = LIB + ".tmp"
-    cmd = [hipcc(), "--offload-arch=gfx950", "-shared", "-fPIC", *objs, "-o", tmp]
-    res = subprocess.run(cmd, capture_output=True, text=True)
-    if res.returncode != 0:
-        raise RuntimeError("link failed:\n" + " ".join(cmd) + "\n" + res.stdout + res.stderr)
-    if verbose:
-        print(" ".join(cmd))
+    error = _failure(*_start([hipcc(), "--offload-arch=gfx950", "-shared", "-fPIC", *objs, "-o", tmp]), verbose)
+    if error:
+        raise RuntimeError("link failed:\n" + error)
     os.replace(tmp, LIB)
-    res = subprocess.run(link_module, capture_output=True, text=True)
-    if res.returncode != 0:
-        raise RuntimeError("link failed:\n" + " ".join(link_module) + "\n" + res.stdout + res.stderr)
-    if verbose:
-        print(" ".join(link_module))
-    os.replace(module_tmp, MODULE)
-    for obj in [*objs, module_obj]:
+    for obj in objs:
         os.remove(obj)
+    if module:
+        module_error = module_error or _failure(*_start(link_module), verbose)
+        if module_error:
+            raise RuntimeError(f"{LIB} is built, the module sv_torch is not:\n" + module_error)
+        os.replace(module_tmp, MODULE)
+        os.remove(module_obj)
     return LIB
 
 
 def is_stale() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(MODULE):
+    built, sources = [LIB], DEPS
+    if has_torch():
+        built, sources = [LIB, MODULE], [*DEPS, MODULE_SRC]
+    if not all(map(os.path.exists, built)):
         return True
-    t = min(os.path.getmtime(LIB), os.path.getmtime(MODULE))
-    return any(os.path.getmtime(d) > t for d in [*DEPS, MODULE_SRC])
+    t = min(map(os.path.getmtime, built))
+    return any(os.path.getmtime(d) > t for d in sources)
 
 
 if __name__ == "__main__":
