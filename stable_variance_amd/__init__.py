@@ -160,14 +160,18 @@ _native = None
 
 def native():
     """The module sv_torch, the short way from ordinary tensors to the library
-    (raises if absent)."""
+    (raises if absent, or made for another torch or Python)."""
     global _native
     if _native is None:
         import importlib.util
 
+        from .build import module_fits, module_tag
+
         capi()  # loads torch and the library
         if not os.path.exists(_MODULE_PATH):
             raise ImportError(f"sv_torch.so is not built ({_MODULE_PATH}); run __graft_entry__.build()")
+        if not module_fits(_MODULE_PATH):
+            raise ImportError(f"{_MODULE_PATH} is not {module_tag()}; run __graft_entry__.build()")
         spec = importlib.util.spec_from_file_location("sv_torch", _MODULE_PATH)
         module = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(module)

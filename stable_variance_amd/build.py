@@ -5,6 +5,7 @@ from __future__ import annotations
 import importlib.util
 import os
 import subprocess
+import sys
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -39,6 +40,19 @@ def hipcc() -> str:
     return "hipcc"
 
 
+def module_tag() -> str:
+    """What the module is made for, as its file says it."""
+    import torch
+
+    return f"sv_torch for torch {torch.__version__}, Python {sys.version_info[0]}.{sys.version_info[1]}"
+
+
+def module_fits(path: str = None) -> bool:
+    """Whether a built module is made for the torch and the Python that run."""
+    with open(path or MODULE, "rb") as f:
+        return module_tag().encode() + b"\0" in f.read()
+
+
 def module_commands(obj: str, out: str):
     """The compile and the link command of the module; the link needs LIB."""
     import sysconfig
@@ -50,7 +64,7 @@ def module_commands(obj: str, out: str):
             os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(hipcc()))), "include"),
             sysconfig.get_paths()["include"]]
     cxx = ["g++", "-O2", "-std=c++17", "-fPIC", "-Wall", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f'-DSV_TORCH_TAG="{module_tag()}"']
     for d in dirs:
         cxx += ["-isystem", d]
     link = ["g++", "-shared", obj, "-L" + OUT_DIR, "-l:" + os.path.basename(LIB), "-L" + os.path.join(root, "lib"),
@@ -125,7 +139,7 @@ def is_stale() -> bool:
     built, sources = [LIB], DEPS
     if has_torch():
         built, sources = [LIB, MODULE], [*DEPS, MODULE_SRC]
-    if not all(map(os.path.exists, built)):
+    if not all(map(os.path.exists, built)) or (MODULE in built and not module_fits()):
         return True
     t = min(map(os.path.getmtime, built))
     return any(os.path.getmtime(d) > t for d in sources)

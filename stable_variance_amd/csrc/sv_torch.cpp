@@ -334,7 +334,11 @@ PyMethodDef methods[] = {
     {nullptr, nullptr, 0, nullptr},
 };
 
-PyModuleDef module = {PyModuleDef_HEAD_INIT, "sv_torch", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
+// The torch and the Python whose headers these are, by which the build and the
+// package know the file: with others it would reach into other layouts.
+const char tag[] = SV_TORCH_TAG;
+
+PyModuleDef module = {PyModuleDef_HEAD_INIT, "sv_torch", tag, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace
 

@@ -4,12 +4,14 @@ import os
 import sys
 
 import pytest
+import torch
 
+import stable_variance_amd as sv
 from stable_variance_amd import build as libbuild
 
 WORKS = """#!/bin/sh
 while [ $# -gt 0 ]; do
-  if [ "$1" = -o ]; then echo built > "$2"; fi
+  if [ "$1" = -o ]; then printf '%s\\0' "$MADE_FOR" > "$2"; fi
   shift
 done
 """
@@ -25,6 +27,7 @@ def tools(tmp_path, monkeypatch):
     monkeypatch.setattr(libbuild, "OUT_DIR", str(out))
     monkeypatch.setattr(libbuild, "LIB", str(out / "libstable_variance.so"))
     monkeypatch.setattr(libbuild, "MODULE", str(out / "sv_torch.so"))
+    monkeypatch.setenv("MADE_FOR", libbuild.module_tag())
 
     def use(hipcc, gxx):
         for name, script in (("hipcc", hipcc), ("g++", gxx)):
@@ -49,6 +52,23 @@ def test_both(tools):
     assert left() == ["libstable_variance.so", "sv_torch.so"] and not libbuild.is_stale()
     os.remove(libbuild.MODULE)
     assert libbuild.is_stale()
+
+
+@pytest.mark.parametrize("version", ["2.9.1", torch.__version__ + "1", torch.__version__[:-1]])
+def test_a_module_for_another_torch_is_stale(tools, monkeypatch, version):
+    tools(WORKS, WORKS)
+    monkeypatch.setenv("MADE_FOR", libbuild.module_tag().replace(torch.__version__, version))
+    libbuild.build()
+    assert libbuild.is_stale()
+    monkeypatch.setattr(sv, "_native", None)
+    monkeypatch.setattr(sv, "_MODULE_PATH", libbuild.MODULE)
+    with pytest.raises(ImportError, match="is not sv_torch for torch"):
+        sv.native()  # and not the loader's error, or a crash
+
+
+def test_the_module_says_what_it_is_made_for():
+    assert libbuild.module_fits()
+    assert sv.native().__doc__ == libbuild.module_tag()
 
 
 @pytest.mark.parametrize("gxx", [WORKS, FAILS, None], ids=["works", "fails", "none"])
