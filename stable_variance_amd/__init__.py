@@ -179,6 +179,31 @@ def native():
     return _native
 
 
+class _GeneralWay:
+    """In the module's place: every call is left to the general way."""
+
+    rms = rms_backward = grad_norm = clip_grad_norm = staticmethod(lambda *_: None)
+
+
+_short_way = None
+
+
+def short_way():
+    """native(), or where it cannot be loaded, which is said once, a stand-in
+    that leaves every call to the general way: that needs the library alone."""
+    global _short_way
+    if _short_way is None:
+        try:
+            _short_way = native()
+        except ImportError as e:
+            import warnings
+
+            capi()  # the library is needed either way
+            warnings.warn(f"the calls take the longer way into the library: {e}", RuntimeWarning, stacklevel=3)
+            _short_way = _GeneralWay
+    return _short_way
+
+
 def _check(status: int) -> None:
     if status != SV_OK:
         msg = capi().sv_last_error_message().decode(errors="replace")

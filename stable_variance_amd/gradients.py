@@ -15,7 +15,7 @@ from operator import attrgetter
 import torch
 from torch.autograd import forward_ad
 
-from . import SvError, _check, capi, native
+from . import SvError, _check, capi, short_way as native
 from .layers import _CODES, _no_tangents, _on, _raw_stream, _stored, _TYPES, _UNSUPPORTED
 
 __all__ = ["grad_norm", "clip_grad_norm"]

@@ -25,7 +25,7 @@ import operator
 import torch
 from torch.autograd import forward_ad
 
-from . import SvError, _check, capi, native
+from . import SvError, _check, capi, short_way as native
 
 __all__ = ["layer_norm", "layer_norm_backward", "rms_norm", "rms_norm_fp8", "rms_norm_backward", "embedding",
            "embedding_backward"]

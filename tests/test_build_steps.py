@@ -2,6 +2,7 @@
 alone, the module that takes torch's tensors to it torch and g++ too."""
 import os
 import sys
+import warnings
 
 import pytest
 import torch
@@ -105,3 +106,28 @@ def test_no_module_without_the_library(tools, hipcc):
     with pytest.raises(RuntimeError, match="hipcc"):
         libbuild.build()
     assert not any(name.endswith(".so") for name in left())
+
+
+def test_the_calls_need_the_library_alone(tools, monkeypatch):
+    # the module absent or for another torch: said once, and the calls go on
+    tools(WORKS, WORKS)
+    monkeypatch.setenv("MADE_FOR", "another")
+    libbuild.build()
+    x, s = torch.zeros(3, 4), torch.zeros(3)
+    for path in (libbuild.MODULE, libbuild.MODULE + ".none"):
+        monkeypatch.setattr(sv, "_native", None)
+        monkeypatch.setattr(sv, "_short_way", None)
+        monkeypatch.setattr(sv, "_MODULE_PATH", path)
+        with pytest.warns(RuntimeWarning, match="longer way"), pytest.raises(ValueError):
+            sv.rms_norm(x)
+        with warnings.catch_warnings():
+            warnings.simplefilter("error")
+            for call in (lambda: sv.rms_norm(x), lambda: sv.rms_norm_fp8(x), lambda: sv.grad_norm([x]),
+                         lambda: sv.rms_norm_backward(x, x, s, x[0]), lambda: sv.clip_grad_norm([x], 1.0)):
+                with pytest.raises(ValueError):  # not on a HIP device: the general way has looked at it
+                    call()
+    monkeypatch.setattr(sv, "_short_way", None)
+    monkeypatch.setattr(sv, "_lib", None)
+    monkeypatch.setattr(sv, "_LIB_PATH", libbuild.LIB + ".none")
+    with pytest.raises(ImportError, match="libstable_variance"):
+        sv.rms_norm(x)
