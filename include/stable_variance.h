@@ -46,7 +46,8 @@
  *   - The call is asynchronous: it enqueues work on `stream` (a hipStream_t;
  *     NULL is the default stream) and returns.  Outputs are valid once the
  *     stream has been synchronised.  Inputs must stay valid until then.
- *   - Calls never throw and never allocate device memory.  They make no
+ *   - Calls never throw and never allocate device memory (sv_clip_grad_norm
+ *     alone takes host memory, freed before it returns).  They make no
  *     memset or copy calls and no host synchronisation, and every counter
  *     they use is reset by the kernels, so a sequence of calls can be
  *     captured once in a HIP graph and replayed.
@@ -72,6 +73,7 @@ typedef int sv_status;
 #define SV_ERR_NO_DEVICE 3        /* no usable HIP device                        */
 #define SV_ERR_HIP 4              /* a HIP runtime call or a launch failed       */
 #define SV_ERR_UNSUPPORTED 5      /* shape outside what the library supports     */
+#define SV_ERR_HOST_MEMORY 6      /* no host memory for the call's own checks    */
 
 /* Version of this ABI (SV_ABI_VERSION of the header the library was built with). */
 int sv_abi_version(void);
@@ -566,6 +568,8 @@ sv_status sv_grad_norm(const void *const *tensors, const int64_t *sizes, const i
  *              place), else what is written must not overlap what is read or
  *              written for any tensor (SV_ERR_INVALID_ARGUMENT)
  *   max_norm   >= 0 (Inf: no limit, nothing is scaled)
+ * The search for overlaps takes 48 bytes of host memory a tensor
+ * (SV_ERR_HOST_MEMORY without them).
  * The other arguments and the workspace as for sv_grad_norm.
  */
 sv_status sv_clip_grad_norm(const void *const *tensors, void *const *out, const int64_t *sizes, const int *dtypes,

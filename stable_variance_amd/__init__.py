@@ -41,7 +41,7 @@ __all__ = ["tree_sum", "var", "var_variant", "capi", "library_path", "SvError", 
 
 SV_OK = 0
 _STATUS = {1: "SV_ERR_INVALID_ARGUMENT", 2: "SV_ERR_WORKSPACE", 3: "SV_ERR_NO_DEVICE", 4: "SV_ERR_HIP",
-           5: "SV_ERR_UNSUPPORTED"}
+           5: "SV_ERR_UNSUPPORTED", 6: "SV_ERR_HOST_MEMORY"}
 
 
 class SvError(RuntimeError):

@@ -17,7 +17,6 @@
 // sum goes to `part`, and a last workgroup adds those up in order: the same
 // bits on every run, no atomics.
 #include <algorithm>
-#include <new>
 #include <stdlib.h>
 
 #include "sv_rms.hpp"
@@ -373,7 +372,7 @@ sv_status sv_clip_grad_norm(const void *const *tensors, void *const *out, const 
     if (sizes[i] && (!out[i] || reinterpret_cast<uintptr_t>(out[i]) % svr::dtype_bytes(dtypes[i])))
       return fail(SV_ERR_INVALID_ARGUMENT, "%s: out %lld is NULL or not aligned to its type", who, (long long)i);
   const int64_t bad = overlap(tensors, out, sizes, dtypes, count);
-  if (bad == -2) return fail(SV_ERR_INVALID_ARGUMENT, "%s: no host memory for %lld tensors", who, (long long)count);
+  if (bad == -2) return fail(SV_ERR_HOST_MEMORY, "%s: no host memory for %lld tensors", who, (long long)count);
   if (bad >= 0)
     return fail(SV_ERR_INVALID_ARGUMENT, "%s: tensor %lld overlaps one that is written", who, (long long)bad);
   st = check_workspace(who, workspace, workspace_bytes, sv_grad_norm_workspace_size(sizes, dtypes, count));

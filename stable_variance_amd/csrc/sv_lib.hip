@@ -2398,6 +2398,7 @@ const char *sv_status_string(sv_status s) {
     case SV_ERR_NO_DEVICE: return "SV_ERR_NO_DEVICE";
     case SV_ERR_HIP: return "SV_ERR_HIP";
     case SV_ERR_UNSUPPORTED: return "SV_ERR_UNSUPPORTED";
+    case SV_ERR_HOST_MEMORY: return "SV_ERR_HOST_MEMORY";
     default: return "SV_ERR_UNKNOWN";
   }
 }
