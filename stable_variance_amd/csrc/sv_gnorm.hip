@@ -382,6 +382,7 @@ sv_status sv_clip_grad_norm(const void *const *tensors, void *const *out, const 
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   float *factor = (float *)workspace;
   launch_norm(tensors, sizes, dtypes, count, max_norm, norm, factor, (double *)((char *)workspace + 256), s);
+  if ((st = check_launch(who)) != SV_OK) return st;  // no factor was written: nothing is scaled
   for_tables<true>(tensors, out, sizes, dtypes, count, [&](const Table<true> &t, const Plan &plan) {
     k_gnorm_scale<<<(unsigned)plan.blocks, THREADS, 0, s>>>(t, plan.units, plan.per, factor);
   });
