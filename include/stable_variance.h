@@ -477,10 +477,10 @@ sv_status sv_embedding_backward(const void *dy, int64_t lddy, const void *ids, i
  * The squares are exact and summed in double, so no finite row overflows or
  * underflows there; rstd itself is a float32 (a root mean square above 2^126
  * makes it subnormal, one below 2^-128 with eps = 0 is beyond it).  A row of
- * zeros gives 0 when eps > 0 (eps = 0 divides zero by zero: NaN).  An Inf in a row gives NaN in its place and
- * 0 in the others, a NaN makes the whole row NaN; no other row changes.  A
- * row's outputs have the same bits on every run and do not depend on the
- * other rows.
+ * zeros gives 0 when eps > 0 (eps = 0 divides zero by zero: NaN).  An Inf in a
+ * row gives NaN in its place and 0 in the others, a NaN makes the whole row
+ * NaN; no other row changes.  A row's outputs have the same bits on every run
+ * and do not depend on the other rows.
  *   dtype        SV_DTYPE_F32, BF16 or F16: of x and y
  *   sum_dtype    of residual and sum: dtype or SV_DTYPE_F32 (dtype when they
  *                are NULL; both are given or neither)

@@ -10,6 +10,8 @@ import sys
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 SRC = os.path.join(HERE, "csrc", "sv_lib.hip")
+# In this order the build guards' search over all assembly is short: they look
+# for every kernel from its start, so many small kernels come first.
 SRCS = [os.path.join(HERE, "csrc", name) for name in (
     "sv_gnorm.hip", "sv_f64.hip", "sv_rms.hip", "sv_rms_grad.hip", "sv_embed.hip", "sv_lib.hip", "sv_norm.hip",
     "sv_rms_fp8.hip", "sv_adn.hip", "sv_adn_folds_9_14.hip", "sv_adn_folds_15_21.hip")]

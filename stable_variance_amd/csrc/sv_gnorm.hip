@@ -116,7 +116,12 @@ __device__ __forceinline__ double sum_squares(const T *p, int64_t n) {
 // they are non-temporal.  Eight waves per SIMD (64 registers) with four chunks
 // a thread in flight; bound by the read.  1.74 GB of bf16: 257 us, 6.8 TB/s
 // (plain loads 293 us, 96 registers 269, one chunk in flight 290); a plain read
-// of them takes 247.  100 MB clipped: 51 us with plain loads, 54 with others.
+// of them takes 247.  Clipping float32 to other buffers, all of it in us, with
+// plain loads and with others: 100 MB 53 and 54, 256 MB 123 and 125, 512 MB 243
+// and 244, 1.34 GB 632 and 634: the sum alone is slower with plain ones (241
+// against 196 at 1.34 GB), and the scaling gets it back.  In place with k = 1,
+// where nothing is read again, plain ones lose: 111 and 99 at 512 MB, 273 and 244
+// at 1.34 GB.
 template <bool AGAIN>
 __global__ __launch_bounds__(THREADS, 8) void k_gnorm_sum(Table<false> t, int64_t units, int64_t per, double *part) {
   __shared__ double lds[THREADS / 64];

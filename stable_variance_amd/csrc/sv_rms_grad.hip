@@ -37,11 +37,15 @@ constexpr int64_t GRAD_RUN = 32;
 // STREAM: what is read is loaded non-temporal, which leaves the last-level
 // cache to dh and its reader.  Measured between kernels that write dsum and dy
 // (with 256 MB of other stores between) and one that reads dh, n = 4096 bf16,
-// all of it in us, with plain loads and so: 4096 rows (100 MB in) 103 and 106;
-// 8192 rows 164 and 153; 16384 rows 281 and 253.
+// all of it in us, with plain loads and so: 4096 rows (96 MB in) 118 and 115,
+// 8192 rows (192 MB) 178 and 168, 10923 rows (256 MB) 224 and 208.  The call by
+// itself, whose inputs the cache may hold from before: 28 and 31, 46 and 52, 74
+// and 64, for 16384 rows 101 and 94.  So it is taken above 192 MB: up to there
+// one of the two gains what the other loses, and at 256 MB both gain.
 // Bound by the three or four streams: 16384 x 4096 bf16 with dsum 89 us and 5
-// for the join, 6.1 TB/s.  5003 x 1531 f16 16 us, 3.0 TB/s: 2.4 rounds of rows
-// over the chip, two waves per SIMD.
+// for the join, 6.1 TB/s; 200000 x 128 bf16 33 us, with dsum 43 (4.7 TB/s).  5003
+// x 1531 f16 16 us, 3.0 TB/s: 2.4 rounds of rows over the chip, two waves per
+// SIMD.
 template <class T, class S, bool SUM, bool STREAM, int L, int K, int FIT>
 __global__ __launch_bounds__(grad_tpb(L, K * svm::chunk_values<T, S>(), svm::chunk_values<T, S>())) void k_rms_grad(
     const T *__restrict__ dy, int64_t lddy, const S *__restrict__ h, int64_t ldh, const S *__restrict__ dsum,
@@ -211,7 +215,10 @@ int64_t grad_blocks(int dtype, int sum_dtype, int64_t rows, int64_t n) {
 
 // ---------------------------------------------------------------- longer rows
 
-// The rows' part of the backward pass for rows of any length.
+// The rows' part of the backward pass for rows of any length: dy and h are read
+// twice here and once more for the columns.  Both parts and the join: 2000 x
+// 12291 bf16 94 us, 2000 x 20000 104 us (2.3 TB/s of what is read and written
+// once), in float32 118 and 186, where 2000 x 12288 bf16 held in registers take 35.
 template <class T, class S>
 __global__ __launch_bounds__(ROW_THREADS) void k_rms_dh_any(const T *dy, int64_t lddy, const S *h, int64_t ldh,
                                                             const S *dsum, int64_t ldds, Rows a, S *dh, int64_t lddh,

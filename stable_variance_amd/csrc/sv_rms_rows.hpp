@@ -12,7 +12,9 @@ using svm::ROW_THREADS;
 using svm::Rows;
 
 // Rows of any length: a workgroup per row, each pass reads the row again (from
-// the cache where it fits).
+// the cache where it fits).  2000 x 40000 bf16 89 us, 3.6 TB/s of what is read
+// and written once (float32 184 us, to 8 bits 83), where 2000 x 32768 held in
+// registers take 59.
 template <class T, class S, bool RES, bool Q>
 __global__ __launch_bounds__(ROW_THREADS) void k_rms_any(const T *x, int64_t ldx, const S *res, int64_t ldr, Rows a,
                                                          T *y, int64_t ldy, S *h, int64_t ldh, Out8 o) {
@@ -115,7 +117,9 @@ constexpr int tpb(int L) { return L <= 128 ? 256 : L; }
 // between a kernel that writes x and one that reads y, with h read after 256
 // MB of other stores, n = 4096 bf16, all of it in us, with h stored plainly,
 // then non-temporal, then the loads so too: 4096 rows 96.7, 96.1, 98.7; 16384
-// rows (256 MB in) 241, 236, 229; 32768 rows 443, 434, 398.
+// rows (256 MB in) 241, 236, 229; 32768 rows 443, 434, 398.  With h read as well,
+// plain loads and others: 8192 rows 172 and 174, 12288 rows 230 and 231, 16384
+// rows 299 and 299 (the kernel by itself 99 and 86).
 // Bound by the read and the write: 16384 x 8192 bf16 with a residual to 8 bits
 // 147 us, 6.4 TB/s, 200000 x 128 bf16 17.6 us, 5.8 TB/s (a copy in torch runs
 // at 4.9-5.4).  Short of that, few rows: 5003 x 1531 f16 to 8 bits 9.8 us, 2.3
@@ -305,8 +309,10 @@ void forward(const void *x, int64_t ldx, const void *residual, int64_t ldr, int 
         k_rms_rows<T, S, RES, Q, decltype(st)::value, L, K, FIT><<<grid, TPB, 0, s>>>(
             (const T *)x, ldx, (const S *)residual, ldr, a, (T *)y, ldy, (S *)sum, ldsum, o);
       };
-      // longer rows of whole chunks only, as the others are bound by more than
-      // the read and every kernel is there once more for it
+      // longer rows of whole chunks only, as every kernel is there once more for
+      // it.  Shorter ones gain nothing: 2000000 x 128 bf16 (512 MB) by itself 203
+      // us with plain loads and 201 so, between a writer and a reader 588 and 599;
+      // 270000 x 1000 221 and 230.  Rows that end inside a chunk were not timed.
       if constexpr (FIT == svr::FIT_CHUNKS && L >= 128) {
         if (stream) return rows(std::true_type{});
       }
