@@ -199,8 +199,8 @@ def short_way():
             import warnings
 
             capi()  # the library is needed either way
-            warnings.warn(f"the calls take the longer way into the library: {e}", RuntimeWarning, stacklevel=3)
             _short_way = _GeneralWay
+            warnings.warn(f"the calls take the longer way into the library: {e}", RuntimeWarning, stacklevel=3)
     return _short_way
 
 

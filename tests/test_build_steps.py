@@ -127,6 +127,13 @@ def test_the_calls_need_the_library_alone(tools, monkeypatch):
                 with pytest.raises(ValueError):  # not on a HIP device: the general way has looked at it
                     call()
     monkeypatch.setattr(sv, "_short_way", None)
+    with warnings.catch_warnings():
+        warnings.simplefilter("error")
+        with pytest.raises(RuntimeWarning):
+            sv.rms_norm(x)
+        with pytest.raises(ValueError):  # also where the warning is made an error
+            sv.rms_norm(x)
+    monkeypatch.setattr(sv, "_short_way", None)
     monkeypatch.setattr(sv, "_lib", None)
     monkeypatch.setattr(sv, "_LIB_PATH", libbuild.LIB + ".none")
     with pytest.raises(ImportError, match="libstable_variance"):
