@@ -488,7 +488,7 @@ sv_status sv_embedding_backward(const void *dy, int64_t lddy, const void *ids, i
  *   eps          >= 0 and finite
  *   y, sum       [rows, n], row strides ldy and ldsum; must not overlap each
  *                other, x or residual
- *   rstd         rows float32 values, may be NULL
+ *   rstd         rows float32 values (aligned to their type), may be NULL
  * Strides, alignment and limits as for sv_layer_norm, and what lies behind
  * the rows of x and residual likewise.  n == 0 gives rstd = NaN.
  */
@@ -522,8 +522,10 @@ sv_status sv_rms_norm_fp8(const void *x, int64_t ldx, const void *residual, int6
  *   dweight_j = sum over the rows of dy_j * xhat_j
  * dh is the gradient of x and of the residual alike.  Every sum's order is
  * fixed by the shape and the types: the same bits on every run, no atomics.
- *   dtype          of dy and dx
+ *   dtype          of dy and dx; strides as for sv_layer_norm, and what lies
+ *                  between the rows of dy, h and dsum likewise
  *   sum_dtype      of h, dsum and dh: dtype or SV_DTYPE_F32
+ *   rstd           rows float32 values (aligned to their type)
  *   dsum           may be NULL (then 0)
  *   dh, dx         the gradient rounded to sum_dtype and to dtype; each may be
  *                  NULL.  They must not overlap each other, dy, h or dsum

@@ -39,6 +39,7 @@ sv_status sv_rms_norm(const void *x, int64_t ldx, const void *residual, int64_t 
                                     sum, ldsum);
   if (st != SV_OK) return st;
   if ((st = svr::check_matrix(who, "y", y, ldy, rows, n, svr::dtype_bytes(dtype))) != SV_OK) return st;
+  if ((st = svr::check_stats(who, "rstd", rstd, rows)) != SV_OK) return st;
   if (rows == 0 || (n == 0 && !rstd)) return ok();
   if ((st = check_device()) != SV_OK) return st;
   (void)hipGetLastError();

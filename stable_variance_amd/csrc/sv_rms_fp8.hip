@@ -23,6 +23,7 @@ sv_status sv_rms_norm_fp8(const void *x, int64_t ldx, const void *residual, int6
     return fail(SV_ERR_INVALID_ARGUMENT, "%s: block = %lld must be %d, or 0 for whole rows", who, (long long)block,
                 BLOCK);
   if ((st = svr::check_matrix(who, "q", q, ldq, rows, n, 1)) != SV_OK) return st;
+  if ((st = svr::check_stats(who, "rstd", rstd, rows)) != SV_OK) return st;
   if (rows > 0 && (n > 0 || block == 0)) {
     if (!scale) return fail(SV_ERR_INVALID_ARGUMENT, "%s: scale is NULL", who);
     if (reinterpret_cast<uintptr_t>(scale) % sizeof(float))

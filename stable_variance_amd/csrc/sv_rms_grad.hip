@@ -389,6 +389,7 @@ sv_status sv_rms_norm_backward(const void *dy, int64_t lddy, const void *h, int6
   if (dx && (st = svr::check_matrix(who, "dx", dx, lddx, rows, n, e)) != SV_OK) return st;
   if (dweight && (st = svr::check_matrix(who, "dweight", dweight, n, 1, n, pe)) != SV_OK) return st;
   if (rows > 0 && n > 0 && !rstd) return fail(SV_ERR_INVALID_ARGUMENT, "%s: rstd is NULL", who);
+  if ((st = svr::check_stats(who, "rstd", rstd, rows)) != SV_OK) return st;
   if (n == 0 || (!dh && !dx && !dweight) || (rows == 0 && !dweight)) return ok();
   const size_t need = sv_rms_norm_backward_workspace_size(rows, n, dtype, sum_dtype);
   if (dweight) {

@@ -375,6 +375,15 @@ inline sv_status check_matrix(const char *who, const char *name, const void *p, 
   return SV_OK;
 }
 
+// A row statistic (one float32 for each row, or NULL): aligned to its type, as
+// a wave that holds one row reads it through the scalar unit, which ignores an
+// address's lowest two bits.
+inline sv_status check_stats(const char *who, const char *name, const float *p, int64_t rows) {
+  if (rows > 0 && reinterpret_cast<uintptr_t>(p) % sizeof(float))
+    return svh::fail(SV_ERR_INVALID_ARGUMENT, "%s: %s is not aligned to its type", who, name);
+  return SV_OK;
+}
+
 // Calls fn(T{}) with the element type of a valid code.
 template <class Fn>
 inline void with_type(int dtype, Fn &&fn) {
