@@ -388,13 +388,14 @@ sv_status sv_adn_sum_f32(const float *x, int64_t n, int fold, float *out, void *
  *                may be NULL (then 1 and 0)
  *   eps          >= 0 and finite
  *   y            [rows, n] of dtype, row stride ldy; must not overlap x
- *   mean, rstd   rows float32 values each, each may be NULL
+ *   mean, rstd   rows float32 values each (aligned to their type), each may be
+ *                NULL
  * Row strides are in values, at least n; x and y need only the alignment of
  * their type (16-byte aligned rows are the fastest).  Where a stride is above
  * n, up to 15 bytes behind a row of x that another row follows may be read
  * (and are not used): they must be readable.  Nothing is written between rows.
- * n == 0 gives mean = rstd = NaN.  n <= 2^27, rows * n <= 2^36 and strides * rows <= 2^40, else
- * SV_ERR_UNSUPPORTED.  No workspace.
+ * n == 0 gives mean = rstd = NaN.  n <= 2^27, rows * n <= 2^36 and
+ * strides * rows <= 2^40, else SV_ERR_UNSUPPORTED.  No workspace.
  */
 sv_status sv_layer_norm(const void *x, int dtype, int64_t rows, int64_t n, int64_t ldx, const void *weight,
                         const void *bias, int param_dtype, double eps, void *y, int64_t ldy, float *mean, float *rstd,
@@ -413,6 +414,7 @@ sv_status sv_layer_norm(const void *x, int dtype, int64_t rows, int64_t n, int64
  * run, no atomics.
  *   dtype          SV_DTYPE_* of dy, x and dx; strides as for sv_layer_norm,
  *                  and what lies between the rows of dy and x likewise
+ *   mean, rstd     rows float32 values each (aligned to their type)
  *   weight         may be NULL (then 1)
  *   param_dtype    type of weight, dweight and dbias: dtype or SV_DTYPE_F32
  *   dx, dweight, dbias  each may be NULL: that gradient is not computed.

@@ -602,6 +602,8 @@ sv_status sv_layer_norm(const void *x, int dtype, int64_t rows, int64_t n, int64
   const size_t pe = svr::dtype_bytes(param_dtype);
   if (weight && (st = svr::check_matrix(who, "weight", weight, n, 1, n, pe)) != SV_OK) return st;
   if (bias && (st = svr::check_matrix(who, "bias", bias, n, 1, n, pe)) != SV_OK) return st;
+  if ((st = svr::check_stats(who, "mean", mean, rows)) != SV_OK) return st;
+  if ((st = svr::check_stats(who, "rstd", rstd, rows)) != SV_OK) return st;
   if (rows == 0) return ok();
   if ((st = check_device()) != SV_OK) return st;
   (void)hipGetLastError();
@@ -648,6 +650,8 @@ sv_status sv_layer_norm_backward(const void *dy, int64_t lddy, const void *x, in
   if (dx && (st = svr::check_matrix(who, "dx", dx, lddx, rows, n, e)) != SV_OK) return st;
   if (rows > 0 && n > 0 && (!mean || !rstd))
     return fail(SV_ERR_INVALID_ARGUMENT, "%s: mean or rstd is NULL", who);
+  if ((st = svr::check_stats(who, "mean", mean, rows)) != SV_OK) return st;
+  if ((st = svr::check_stats(who, "rstd", rstd, rows)) != SV_OK) return st;
   if (n == 0 || (!dx && !dweight && !dbias)) return ok();
   const bool cols = dweight || dbias;
   if (!cols && rows == 0) return ok();
